@@ -20,6 +20,7 @@ from . import build as _build
 __all__ = ["SpffnError", "Layer", "AttnLayer", "attn_step_kernel_launches", "decode", "decode_tables", "decode_kernel_launches", "forward_noalloc",
            "reorder", "reorder_dealt", "permute_rows", "permute_vector", "set_trace", "trace_marks",
            "set_l2_hot_rows", "l2_hot_rows", "set_union_stack", "union_stack",
+           "norm_quant", "quantize_rows", "Linear8", "Rope", "KvCache4", "rope_frequencies",
            "workspace_bytes", "library", "F16", "BF16"]
 
 F16, BF16 = 0, 1
@@ -33,7 +34,11 @@ EXPORTS = ("spffn_workspace_bytes", "spffn_create", "spffn_destroy", "spffn_pred
            "spffn_decode_lookahead", "spffn_layer_table", "spffn_decode_tables", "spffn_set_wait_test", "spffn_set_l2_hot_rows", "spffn_l2_hot_rows",
            "spffn_set_union_stack", "spffn_union_stack",
            "spffn_attn_workspace_bytes", "spffn_attn_create", "spffn_attn_destroy", "spffn_attn_reset",
-           "spffn_attn_step", "spffn_attn_cache", "spffn_attn_step_kernel_launches", "spffn_attn_last_device_error")
+           "spffn_attn_step", "spffn_attn_cache", "spffn_attn_step_kernel_launches", "spffn_attn_last_device_error",
+           "spffn_norm_quant", "spffn_quantize_rows", "spffn_mm8_workspace_bytes", "spffn_mm8_create",
+           "spffn_mm8_destroy", "spffn_mm8_forward", "spffn_mm8_last_device_error", "spffn_rope_frequencies",
+           "spffn_kv4_pool_bytes", "spffn_kv4_workspace_bytes", "spffn_kv4_create", "spffn_kv4_destroy",
+           "spffn_kv4_append", "spffn_kv4_attend", "spffn_kv4_read", "spffn_kv4_last_device_error")
 
 
 class SpffnError(RuntimeError):
@@ -66,6 +71,21 @@ class AttnCacheView(ctypes.Structure):
                 ("t", ctypes.c_void_p)]
 
 
+class Mm8Config(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
+class Mm8Weights(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("W", "w_scale", "bias")]
+
+
+class Kv4Config(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("pages", "page_size", "nh", "kvh", "dh", "max_seqs", "max_tokens", "dtype",
+                                               "rope_dim", "rope_interleaved")] + [
+        ("rope_amplitude", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
 _lib = None
 
 
@@ -83,6 +103,7 @@ def library(path: Optional[str] = None):
                 raise RuntimeError("libspffn.so is missing and could not be built: %s" % e) from e
     lib = ctypes.CDLL(so)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    i64, f32, f64 = ctypes.c_int64, ctypes.c_float, ctypes.c_double
     st = ctypes.c_int
     sig = {
         "spffn_workspace_bytes": (sz, [ctypes.POINTER(Config)]),
@@ -122,6 +143,22 @@ def library(path: Optional[str] = None):
         "spffn_attn_cache": (st, [vp, ctypes.POINTER(AttnCacheView)]),
         "spffn_attn_step_kernel_launches": (i32, []),
         "spffn_attn_last_device_error": (st, [vp, ctypes.POINTER(ctypes.c_uint32), vp]),
+        "spffn_norm_quant": (st, [i32, i32, i32, vp, i64, vp, i64, i32, vp, f32, vp, i64, vp, i64, vp, vp]),
+        "spffn_quantize_rows": (st, [i32, i32, i32, vp, i64, i32, vp, i64, vp, vp]),
+        "spffn_mm8_workspace_bytes": (sz, [ctypes.POINTER(Mm8Config)]),
+        "spffn_mm8_create": (st, [ctypes.POINTER(Mm8Config), ctypes.POINTER(Mm8Weights), vp, sz, ctypes.POINTER(vp)]),
+        "spffn_mm8_destroy": (st, [vp]),
+        "spffn_mm8_forward": (st, [vp, vp, i64, vp, i32, vp, i64, vp]),
+        "spffn_mm8_last_device_error": (st, [vp, ctypes.POINTER(ctypes.c_uint32), vp]),
+        "spffn_rope_frequencies": (st, [i32, f64, i32, f64, f64, ctypes.POINTER(f64), ctypes.POINTER(f32)]),
+        "spffn_kv4_pool_bytes": (sz, [ctypes.POINTER(Kv4Config)]),
+        "spffn_kv4_workspace_bytes": (sz, [ctypes.POINTER(Kv4Config)]),
+        "spffn_kv4_create": (st, [ctypes.POINTER(Kv4Config), vp, sz, vp, vp, sz, ctypes.POINTER(vp)]),
+        "spffn_kv4_destroy": (st, [vp]),
+        "spffn_kv4_append": (st, [vp, vp, i64, vp, i64, vp, i64, i32, vp, i64, i32, vp, vp, i32, vp, i64, vp]),
+        "spffn_kv4_attend": (st, [vp, vp, i64, i32, vp, i64, i32, vp, vp, i32, f32, vp, i64, vp]),
+        "spffn_kv4_read": (st, [vp, vp, i32, vp, vp, vp]),
+        "spffn_kv4_last_device_error": (st, [vp, ctypes.POINTER(ctypes.c_uint32), vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -432,3 +469,288 @@ def permute_rows(src, dst, perm, stream=None):
 def permute_vector(src, dst, perm, stream=None):
     _check(library().spffn_permute_vector(_p(src), _p(dst), src.numel(), _p(perm), _stream(stream)),
            "spffn_permute_vector")
+
+
+# ---- the dense half of a batched decode block (include/spffn_block.h) -----------------------
+
+def _on(device: int, *tensors):
+    """Every tensor (None allowed) lives on CUDA device `device`."""
+    if device < 0:
+        raise TypeError("expected CUDA tensors")
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("expected a CUDA tensor on device %d, got one on %s" % (device, t.device))
+
+
+def _rows(t, what: str, dtype, T=None, d=None):
+    """Row stride of a 2-D tensor whose rows are contiguous; checks its type and shape."""
+    if t.dim() != 2 or (T is not None and t.shape[0] != T) or (d is not None and t.shape[1] != d):
+        raise ValueError("%s: expected shape [%s, %s], got %s" % (what, T, d, tuple(t.shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s: rows must be contiguous" % what)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(t, what: str, dtype, n: int):
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError("%s: expected shape [%d], got %s" % (what, n, tuple(t.shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError("%s must be contiguous" % what)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(device: int, stream, name: str, fn, *args):
+    """fn(*args, stream) with `device` current; `stream` defaults to that device's current stream."""
+    import torch
+    if torch.cuda.current_device() == device:
+        _check(fn(*args, _stream(stream)), name)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)), name)
+
+
+def norm_quant(x, y, g, x_out, q, scale, eps: float = 1e-6, stream=None):
+    """Residual addition, RMS norm and 8-bit rows (spffn_norm_quant): ``u = x + y``, ``x_out = u`` in the
+    storage type, ``q [T, d]`` int8 and ``scale [T]`` fp32 with ``q scale`` the normalised row times ``g``.
+    ``x [T, d]`` float16 or bfloat16; ``y [T, d]`` of that type, float32 or None; ``g [d]`` or None; ``x_out``
+    may be ``x`` (or ``y`` of the same type) or None."""
+    import torch
+    T, d = x.shape
+    code, dev = _dtype_code(x), x.get_device()
+    ldx = _rows(x, "x", x.dtype)
+    y_f32 = y is not None and y.dtype == torch.float32
+    ldy = 0 if y is None else _rows(y, "y", torch.float32 if y_f32 else x.dtype, T, d)
+    ldo = 0 if x_out is None else _rows(x_out, "x_out", x.dtype, T, d)
+    ldq = _rows(q, "q", torch.int8, T, d)
+    _vector(scale, "scale", torch.float32, T)
+    if g is not None:
+        _vector(g, "g", x.dtype, d)
+    _on(dev, x, y, g, x_out, q, scale)
+    _call(dev, stream, "spffn_norm_quant", library().spffn_norm_quant, T, d, code, x.data_ptr(), ldx, _ptr(y), ldy,
+          y_f32, _ptr(g), eps, _ptr(x_out), ldo, q.data_ptr(), ldq, scale.data_ptr())
+
+
+def quantize_rows(x, q, scale, stream=None):
+    """8-bit rows with a scale each (spffn_quantize_rows): ``x [T, d]`` float16, bfloat16 or float32 to
+    ``q [T, d]`` int8 and ``scale [T]`` fp32.  Weights ``[N, K]`` get their scales per channel this way."""
+    import torch
+    T, d = x.shape
+    f32 = x.dtype == torch.float32
+    code, dev = F16 if f32 else _dtype_code(x), x.get_device()
+    ldx, ldq = _rows(x, "x", x.dtype), _rows(q, "q", torch.int8, T, d)
+    _vector(scale, "scale", torch.float32, T)
+    _on(dev, x, q, scale)
+    _call(dev, stream, "spffn_quantize_rows", library().spffn_quantize_rows, T, d, code, x.data_ptr(), ldx, f32,
+          q.data_ptr(), ldq, scale.data_ptr())
+
+
+class Linear8:
+    """A product with 8-bit weights (wraps an ``spffn_mm8_ctx``): ``y = round(scale[t] w_scale[n] sum_k q[t][k]
+    W[n][k] + bias[n])`` with exact integer sums.
+
+    ``W [N, K]`` int8 CUDA tensor, contiguous, K % 16 == 0; ``w_scale [N]`` fp32; ``bias [N]`` of ``dtype`` or
+    None; ``dtype`` (torch.float16 or torch.bfloat16) is the output's type; ``max_tokens`` the most rows of a call.
+    """
+
+    def __init__(self, W, w_scale, bias=None, max_tokens: int = 256, dtype=None, workspace=None):
+        import torch
+        self.out_dtype = dtype if dtype is not None else bias.dtype if bias is not None else torch.float16
+        self.N, self.K = (int(v) for v in W.shape)
+        self.max_tokens = int(max_tokens)
+        if _rows(W, "W", torch.int8) != self.K:
+            raise ValueError("W must be contiguous")
+        _vector(w_scale, "w_scale", torch.float32, self.N)
+        if bias is not None:
+            _vector(bias, "bias", self.out_dtype, self.N)
+        self.device = W.get_device()
+        code = {torch.float16: F16, torch.bfloat16: BF16}.get(self.out_dtype)
+        if code is None:
+            raise TypeError("dtype must be float16 or bfloat16, got %s" % self.out_dtype)
+        _on(self.device, w_scale, bias)
+        self.cfg = Mm8Config(self.K, self.N, self.max_tokens, code, 0)
+        self._keep = [W, w_scale, bias]
+        self.weights = Mm8Weights(_ptr(W), _ptr(w_scale), _ptr(bias))
+        with torch.cuda.device(self.device):
+            need = int(library().spffn_mm8_workspace_bytes(ctypes.byref(self.cfg)))
+            if need == 0:
+                raise SpffnError(ERR_INVALID_ARG, "spffn_mm8_workspace_bytes (bad shape)")
+            if workspace is None:
+                workspace = torch.zeros(need, dtype=torch.uint8, device=W.device)
+            self.workspace = workspace
+            ctx = ctypes.c_void_p()
+            _check(library().spffn_mm8_create(ctypes.byref(self.cfg), ctypes.byref(self.weights), _p(workspace),
+                                              workspace.numel(), ctypes.byref(ctx)), "spffn_mm8_create")
+        self.ctx = ctx
+
+    def close(self):
+        if getattr(self, "ctx", None):
+            library().spffn_mm8_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def forward(self, q, scale, y, stream=None):
+        """``q [T, K]`` int8 and ``scale [T]`` fp32 (as norm_quant leaves them) to ``y [T, N]``."""
+        import torch
+        T = q.shape[0]
+        ldq, ldy = _rows(q, "q", torch.int8, T, self.K), _rows(y, "y", self.out_dtype, T, self.N)
+        _vector(scale, "scale", torch.float32, T)
+        _on(self.device, q, scale, y)
+        _call(self.device, stream, "spffn_mm8_forward", library().spffn_mm8_forward, self.ctx, q.data_ptr(), ldq,
+              scale.data_ptr(), T, y.data_ptr(), ldy)
+
+    def last_device_error(self, stream=None):
+        code = ctypes.c_uint32(0)
+        s = library().spffn_mm8_last_device_error(self.ctx, ctypes.byref(code), _stream(stream))
+        return s, int(code.value)
+
+
+ROPE_SCALINGS = ("plain", "linear", "ntk", "parts")
+
+
+def rope_frequencies(dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, original_len: float = 0.0):
+    """(radians per position of the dim / 2 rotated pairs as a float64 numpy array, amplitude) for the long-context
+    scalings of spffn_rope_frequencies: "plain", "linear", "ntk", "parts"."""
+    out, amp = np.empty(max(dim // 2, 1), dtype=np.float64), ctypes.c_float(1.0)
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % (ROPE_SCALINGS,))
+    _check(library().spffn_rope_frequencies(int(dim), float(base), ROPE_SCALINGS.index(scaling), float(factor), float(original_len),
+                                            out.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), ctypes.byref(amp)),
+           "spffn_rope_frequencies")
+    return out, float(amp.value)
+
+
+class Rope:
+    """Rotary positions of a cache: ``freqs`` (float64 CUDA tensor [dim / 2], radians per position, or a numpy array
+    from rope_frequencies), pairs ``(2i, 2i + 1)`` if ``interleaved`` else ``(i, i + dim / 2)`` of the first dim dims."""
+
+    def __init__(self, freqs, interleaved: bool = False, amplitude: float = 1.0):
+        import torch
+        self.freqs = torch.from_numpy(np.ascontiguousarray(freqs, dtype=np.float64)).cuda() if isinstance(freqs, np.ndarray) else freqs
+        _vector(self.freqs, "freqs", torch.float64, self.freqs.numel())
+        self.interleaved, self.amplitude = bool(interleaved), float(amplitude)
+
+
+class KvCache4:
+    """A paged cache of keys and values in 4 bits (wraps an ``spffn_kv4_ctx``): append with rotary positions, attend,
+    read back.  The pool (uint8 CUDA tensor, allocated here when not given) has pages x page_size tokens of kvh heads of
+    dh dims; ``max_seqs`` and ``max_tokens`` bound the sequences and new tokens of a call.
+
+    The batch of a call: ``table [B, width]`` int32 pages of each sequence, ``lens [B]`` int32 lengths with the new
+    tokens included, ``start [B + 1]`` int32 first rows of the sequences' new tokens, or None for one token each.
+    """
+
+    def __init__(self, pages: int, page_size: int, nh: int, kvh: int, dh: int, dtype, max_seqs: int, max_tokens: int,
+                 rope: Optional[Rope] = None, pool=None, workspace=None, device=None):
+        import torch
+        code = {torch.float16: F16, torch.bfloat16: BF16}.get(dtype)
+        if code is None:
+            raise TypeError("dtype must be float16 or bfloat16, got %s" % dtype)
+        self.pages, self.page_size, self.nh, self.kvh, self.dh, self.dtype = int(pages), int(page_size), int(nh), int(kvh), int(dh), dtype
+        self.rope = rope
+        self.cfg = Kv4Config(self.pages, self.page_size, self.nh, self.kvh, self.dh, int(max_seqs), int(max_tokens), code,
+                             0 if rope is None else 2 * rope.freqs.numel(), rope is not None and rope.interleaved,
+                             1.0 if rope is None else rope.amplitude, 0)
+        device = pool.device if pool is not None else torch.device("cuda" if device is None else device)
+        with torch.cuda.device(device):
+            size = int(library().spffn_kv4_pool_bytes(ctypes.byref(self.cfg)))
+            need = int(library().spffn_kv4_workspace_bytes(ctypes.byref(self.cfg)))
+            if size == 0 or need == 0:
+                raise SpffnError(ERR_INVALID_ARG, "spffn_kv4_pool_bytes (bad shape)")
+            if pool is None:
+                pool = torch.zeros(size, dtype=torch.uint8, device=device)
+            if workspace is None:
+                workspace = torch.zeros(need, dtype=torch.uint8, device=device)
+            self.device = pool.get_device()
+            _on(self.device, pool, workspace, None if rope is None else rope.freqs)
+            self.pool, self.workspace = pool, workspace
+            ctx = ctypes.c_void_p()
+            _check(library().spffn_kv4_create(ctypes.byref(self.cfg), _p(pool), pool.numel() * pool.element_size(),
+                                              None if rope is None else rope.freqs.data_ptr(), _p(workspace),
+                                              workspace.numel(), ctypes.byref(ctx)), "spffn_kv4_create")
+        self.ctx = ctx
+
+    def close(self):
+        if getattr(self, "ctx", None):
+            library().spffn_kv4_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _heads(self, t, what: str, T: int, heads: int):
+        """Row stride of [T, heads, dh] (or [T, heads * dh]) whose rows are contiguous."""
+        if t.dim() == 3:
+            if t.shape != (T, heads, self.dh) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.dh):
+                raise ValueError("%s: expected [%d, %d, %d] with contiguous rows, got %s, strides %s" % (
+                    what, T, heads, self.dh, tuple(t.shape), t.stride()))
+            if t.dtype != self.dtype:
+                raise TypeError("%s: expected %s, got %s" % (what, self.dtype, t.dtype))
+            return t.stride(0) if T > 1 else heads * self.dh
+        return _rows(t, what, self.dtype, T, heads * self.dh)
+
+    def _batch(self, table, lens, start):
+        import torch
+        B = lens.shape[0]
+        ldt = _rows(table, "table", torch.int32, B)
+        _vector(lens, "lens", torch.int32, B)
+        if start is not None:
+            _vector(start, "start", torch.int32, B + 1)
+        _on(self.device, table, lens, start)
+        return table.data_ptr(), ldt, table.shape[1], lens.data_ptr(), _ptr(start), B
+
+    def append(self, q, k, v, table, lens, start=None, q_out=None, stream=None):
+        """Rotate ``q [T, nh, dh]`` into ``q_out`` (may be ``q``; both None to leave it out) and append ``k, v
+        [T, kvh, dh]``, k rotated, at their sequences' positions."""
+        T = k.shape[0]
+        ldk, ldv = self._heads(k, "k", T, self.kvh), self._heads(v, "v", T, self.kvh)
+        ldq, ldo = (0, 0) if q is None else (self._heads(q, "q", T, self.nh), 0)
+        if q_out is not None:
+            ldo = self._heads(q_out, "q_out", T, self.nh)
+        batch = self._batch(table, lens, start)
+        _on(self.device, q, k, v, q_out)
+        _call(self.device, stream, "spffn_kv4_append", library().spffn_kv4_append, self.ctx, _ptr(q), ldq, k.data_ptr(),
+              ldk, v.data_ptr(), ldv, T, *batch, _ptr(q_out), ldo)
+
+    def attend(self, q, table, lens, start=None, out=None, scale: Optional[float] = None, stream=None):
+        """Attention of the new tokens' ``q [T, nh, dh]`` over their sequences' cached positions up to their own, into
+        ``out [T, nh, dh]``; ``scale`` defaults to 1 / sqrt(dh)."""
+        T = q.shape[0]
+        ldq, ldo = self._heads(q, "q", T, self.nh), self._heads(out, "out", T, self.nh)
+        batch = self._batch(table, lens, start)
+        _on(self.device, q, out)
+        _call(self.device, stream, "spffn_kv4_attend", library().spffn_kv4_attend, self.ctx, q.data_ptr(), ldq, T, *batch,
+              self.dh ** -0.5 if scale is None else scale, out.data_ptr(), ldo)
+
+    def read(self, pages, K, V, stream=None):
+        """The cached values of ``pages [n]`` (int32) into ``K, V [n, page_size, kvh, dh]``."""
+        import torch
+        n = pages.shape[0]
+        _vector(pages, "pages", torch.int32, n)
+        for t, what in ((K, "K"), (V, "V")):
+            if t.shape != (n, self.page_size, self.kvh, self.dh) or not t.is_contiguous():
+                raise ValueError("%s: expected a contiguous %s, got %s" % (what, (n, self.page_size, self.kvh, self.dh), tuple(t.shape)))
+            if t.dtype != self.dtype:
+                raise TypeError("%s: expected %s, got %s" % (what, self.dtype, t.dtype))
+        _on(self.device, pages, K, V)
+        _call(self.device, stream, "spffn_kv4_read", library().spffn_kv4_read, self.ctx, pages.data_ptr(), n, K.data_ptr(),
+              V.data_ptr())
+
+    def last_device_error(self, stream=None):
+        code = ctypes.c_uint32(0)
+        s = library().spffn_kv4_last_device_error(self.ctx, ctypes.byref(code), _stream(stream))
+        return s, int(code.value)

@@ -48,6 +48,9 @@ spffn_status cuda_status(cudaError_t e) {
 
 }  // namespace
 
+spffn_status spffn::record_cuda(cudaError_t e) { return cuda_status(e); }
+int spffn::current_sms() { return device_sms(); }
+
 extern "C" {
 
 const char* spffn_last_cuda_error_string(void) {

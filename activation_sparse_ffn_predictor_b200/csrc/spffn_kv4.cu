@@ -1,0 +1,328 @@
+// The paged 4-bit cache: contexts, appending with rotary positions, reading back
+// (declarations and the block format in include/spffn_block.h).
+#include <cmath>
+#include <new>
+#include "spffn_kv4.cuh"
+
+namespace spffn {
+namespace kv4 {
+namespace {
+
+struct AppendParams {
+    const void *q, *k, *v;
+    void* q_out;
+    int64_t ldq, ldk, ldv, ldqo;
+    uint8_t* pool;
+    const double* freqs;
+    float amp;
+    int nh, kvh, dh, rd, inter;
+    Batch b;
+};
+
+// codes of 8 dims as 4 bytes, low 4 bits first
+__device__ __forceinline__ uint32_t pack8(const float* x, float step, float zero) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float c = step > 0.f ? rintf(__fdiv_rn(__fsub_rn(x[i], zero), step)) : 0.f;
+        w |= (uint32_t)(int)fminf(fmaxf(c, 0.f), 15.f) << (4 * i);
+    }
+    return w;
+}
+
+__device__ __forceinline__ float f16_value(float v) {      // rounded to fp16, kept finite
+    return __half2float(__float2half_rn(fminf(fmaxf(v, -65504.f), 65504.f)));
+}
+
+// One CTA per (row, slice of its heads); 8 dims of a head per thread, so a group of 32 dims
+// is four neighbouring lanes.
+template <typename T>
+__global__ void __launch_bounds__(256) k_append(const AppendParams p) {
+    __shared__ float cs[128], sn[128];
+    const int t = blockIdx.x;
+    const int s = seq_of_row(p.b, t);
+    if (s < 0) return;
+    const Seq sq = seq_of(p.b, s);
+    if (!sq.ok || t < sq.row0 || t >= sq.row0 + sq.n) return;
+    const int pos = sq.len - sq.n + (t - sq.row0);
+    const int hrd = p.rd >> 1;
+    for (int i = threadIdx.x; i < hrd; i += blockDim.x) {
+        double a = (double)pos * p.freqs[i], si, co;
+        sincos(a, &si, &co);
+        cs[i] = (float)(co * (double)p.amp);
+        sn[i] = (float)(si * (double)p.amp);
+    }
+    __syncthreads();
+    const int page = p.b.table[(int64_t)s * p.b.ldt + pos / p.b.page];
+    const bool paged = page >= 0 && page < p.b.pages;
+    if (!paged && threadIdx.x == 0 && blockIdx.y == 0) latch(p.b.err, ERR_PAGE_RANGE);
+    const int vph = p.dh >> 3, ng = p.dh >> 5;              // pieces of 8 dims and groups of a head
+    const int heads = (p.q ? p.nh : 0) + 2 * p.kvh, q_heads = p.q ? p.nh : 0;
+    const int tok = pos % p.b.page, blk = tok >> 4;
+    const int items = heads * vph;
+    // whole warps go round together: lanes past the end repeat the last item and store nothing
+    for (int it0 = blockIdx.y * blockDim.x + (threadIdx.x & ~31); it0 < items; it0 += gridDim.y * blockDim.x) {
+        const bool live = it0 + (threadIdx.x & 31) < items;
+        const int it = live ? it0 + (threadIdx.x & 31) : items - 1;
+        const int h = it / vph, e0 = (it % vph) * 8;
+        const int kind = h < q_heads ? 0 : h < q_heads + p.kvh ? 1 : 2;
+        const int hh = kind == 0 ? h : kind == 1 ? h - q_heads : h - q_heads - p.kvh;
+        const T* x = kind == 0 ? static_cast<const T*>(p.q) + t * p.ldq
+                               : kind == 1 ? static_cast<const T*>(p.k) + t * p.ldk : static_cast<const T*>(p.v) + t * p.ldv;
+        x += (int64_t)hh * p.dh;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = e0 + i;
+            float a = DT<T>::f(x[e]);
+            if (kind < 2 && e < p.rd) {
+                const int f = p.inter ? e >> 1 : e < hrd ? e : e - hrd;
+                const bool second = p.inter ? e & 1 : e >= hrd;
+                const float o = DT<T>::f(x[p.inter ? e ^ 1 : second ? e - hrd : e + hrd]);
+                a = second ? __fadd_rn(__fmul_rn(a, cs[f]), __fmul_rn(o, sn[f]))
+                           : __fsub_rn(__fmul_rn(a, cs[f]), __fmul_rn(o, sn[f]));
+            }
+            v[i] = a;
+        }
+        __syncwarp();        // q_out may be q: the loads of a head's lanes (one warp) come before the stores
+        if (kind == 0 && live) {
+            T* o = static_cast<T*>(p.q_out) + t * p.ldqo + (int64_t)hh * p.dh + e0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = DT<T>::r(v[i]);
+        }
+        float lo = v[0], hi = v[0], bad = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo = fminf(lo, v[i]);
+            hi = fmaxf(hi, v[i]);
+            bad += v[i] * 0.f;
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            bad += __shfl_xor_sync(0xffffffffu, bad, o);
+        }
+        const float zero = f16_value(lo), step = bad == 0.f ? f16_value(__fdiv_rn(__fsub_rn(hi, lo), 15.f)) : __int_as_float(0x7fc00000);
+        const uint32_t w = pack8(v, step, zero);
+        if (!paged || !live || kind == 0) continue;
+        const int g = e0 >> 5, c = (e0 & 31) >> 3, lt = tok & 15;
+        uint8_t* rec = p.pool + (((int64_t)page * p.kvh + hh) * (p.b.page >> 4) + blk) * (640 * ng);
+        auto put = [&](auto tag) {
+            using L = Blk<decltype(tag)::value>;
+            if (kind == 1) *reinterpret_cast<uint32_t*>(rec + L::k(lt, g, c)) = w;
+            else {
+                *reinterpret_cast<uint16_t*>(rec + L::v(lt, g, 2 * c)) = (uint16_t)w;
+                *reinterpret_cast<uint16_t*>(rec + L::v(lt, g, 2 * c + 1)) = (uint16_t)(w >> 16);
+            }
+            if (c == 0) {
+                *reinterpret_cast<__half*>(rec + (kind == 1 ? L::ks(lt, g) : L::vs(lt, g))) = __float2half_rn(step);
+                *reinterpret_cast<__half*>(rec + (kind == 1 ? L::kz(lt, g) : L::vz(lt, g))) = __float2half_rn(zero);
+            }
+        };
+        if (ng == 2) put(std::integral_constant<int, 2>());
+        else if (ng == 4) put(std::integral_constant<int, 4>());
+        else put(std::integral_constant<int, 8>());
+    }
+}
+
+// 8 values of one (page of the list, kv head, token) per thread
+template <typename T, int NG>
+__global__ void __launch_bounds__(256) k_read(const uint8_t* pool, const int32_t* ids, int64_t items, int kvh, int page,
+                                              int pages, T* K, T* V, uint32_t* err) {
+    using L = Blk<NG>;
+    const int64_t it = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (it >= items) return;
+    const int e0 = (int)(it % (4 * NG)) * 8, tok = (int)(it / (4 * NG) / kvh % page), h = (int)(it / (4 * NG) % kvh);
+    const int64_t i = it / (4 * NG) / kvh / page;
+    const int id = ids[i];
+    if (id < 0 || id >= pages) {
+        if (e0 == 0) latch(err, ERR_PAGE_RANGE);
+        return;
+    }
+    const uint8_t* rec = pool + (((int64_t)id * kvh + h) * (page >> 4) + (tok >> 4)) * L::kBytes;
+    const int lt = tok & 15, g = e0 >> 5, c = (e0 & 31) >> 3;
+    auto half_at = [&](int o) { return __half2float(*reinterpret_cast<const __half*>(rec + o)); };
+    const uint32_t kw = *reinterpret_cast<const uint32_t*>(rec + L::k(lt, g, c));
+    const uint32_t vw = *reinterpret_cast<const uint16_t*>(rec + L::v(lt, g, 2 * c)) |
+                        ((uint32_t)*reinterpret_cast<const uint16_t*>(rec + L::v(lt, g, 2 * c + 1)) << 16);
+    const float ks = half_at(L::ks(lt, g)), kz = half_at(L::kz(lt, g)), vs = half_at(L::vs(lt, g)), vz = half_at(L::vz(lt, g));
+    T ko[8], vo[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        ko[j] = DT<T>::r(fmaf((float)((kw >> (4 * j)) & 15u), ks, kz));
+        vo[j] = DT<T>::r(fmaf((float)((vw >> (4 * j)) & 15u), vs, vz));
+    }
+    *reinterpret_cast<uint4*>(K + it * 8) = *reinterpret_cast<const uint4*>(ko);
+    *reinterpret_cast<uint4*>(V + it * 8) = *reinterpret_cast<const uint4*>(vo);
+}
+
+bool valid(const spffn_kv4_config* c) {
+    if (!c || c->flags != 0 || c->pages < 1 || c->pages > (1 << 24)) return false;
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128 && c->page_size != 256) return false;
+    if (c->nh < 1 || c->nh > 1024 || c->kvh < 1 || c->nh % c->kvh || c->nh / c->kvh > 64) return false;
+    if (c->dh != 64 && c->dh != 128 && c->dh != 256) return false;
+    if (c->max_seqs < 1 || c->max_seqs > 4096 || c->max_tokens < 1 || c->max_tokens > 65536) return false;
+    if (c->dtype != SPFFN_F16 && c->dtype != SPFFN_BF16) return false;
+    if (c->rope_dim < 0 || c->rope_dim > c->dh || c->rope_dim % 2) return false;
+    if (c->rope_dim && !(std::isfinite(c->rope_amplitude))) return false;
+    return true;
+}
+
+bool valid_batch(const spffn_kv4_ctx* c, int T, const int32_t* table, int64_t ldt, int width, const int32_t* lens,
+                 const int32_t* start, int B) {
+    if (B < 0 || B > c->cfg.max_seqs || T < 0 || T > c->cfg.max_tokens || width < 0) return false;
+    if (B == 0 || T == 0) return true;
+    return lens && aligned_to(lens, 4) && aligned_to(start, 4) && aligned_to(table, 4) && table && width >= 1 && ldt >= width &&
+           (start || T >= B);
+}
+
+Batch batch_of(const spffn_kv4_ctx* c, int T, const int32_t* table, int64_t ldt, int width, const int32_t* lens,
+               const int32_t* start, int B) {
+    Batch b;
+    b.table = table;
+    b.lens = lens;
+    b.start = start;
+    b.ldt = ldt;
+    b.width = width;
+    b.B = B;
+    b.T = T;
+    b.page = c->cfg.page_size;
+    b.page_log = 0;
+    while ((1 << b.page_log) < b.page) ++b.page_log;
+    b.pages = c->cfg.pages;
+    b.err = c->err();
+    return b;
+}
+
+}  // namespace
+}  // namespace kv4
+}  // namespace spffn
+
+using namespace spffn;
+using namespace spffn::kv4;
+
+extern "C" {
+
+spffn_status spffn_rope_frequencies(int32_t rope_dim, double base, int32_t scaling, double factor, double original_len,
+                                    double* out, float* amplitude) {
+    if (rope_dim < 2 || rope_dim % 2 || !out || !(base > 0) || !std::isfinite(base)) return SPFFN_ERR_INVALID_ARG;
+    if (scaling < SPFFN_ROPE_PLAIN || scaling > SPFFN_ROPE_PARTS) return SPFFN_ERR_INVALID_ARG;
+    if (scaling != SPFFN_ROPE_PLAIN && !(factor >= 1 && std::isfinite(factor))) return SPFFN_ERR_INVALID_ARG;
+    if (scaling == SPFFN_ROPE_NTK && rope_dim < 4) return SPFFN_ERR_INVALID_ARG;
+    if (scaling == SPFFN_ROPE_PARTS && !(original_len >= 1 && std::isfinite(original_len))) return SPFFN_ERR_INVALID_ARG;
+    if (scaling == SPFFN_ROPE_NTK) base *= std::pow(factor, (double)rope_dim / (rope_dim - 2));
+    for (int i = 0; i < rope_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rope_dim);
+        if (scaling == SPFFN_ROPE_LINEAR) f /= factor;
+        if (scaling == SPFFN_ROPE_PARTS) {
+            const double turns = original_len * f / (2 * 3.14159265358979323846);
+            const double keep = std::min(1.0, std::max(0.0, (turns - 1.0) / 31.0));
+            f = f / factor * (1 - keep) + f * keep;
+        }
+        out[i] = f;
+    }
+    if (amplitude) *amplitude = scaling == SPFFN_ROPE_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+    return SPFFN_OK;
+}
+
+size_t spffn_kv4_pool_bytes(const spffn_kv4_config* c) {
+    if (!valid(c)) return 0;
+    return (size_t)c->pages * c->kvh * (c->page_size / 16) * (20 * c->dh);
+}
+
+size_t spffn_kv4_workspace_bytes(const spffn_kv4_config* c) { return valid(c) ? layout(*c, current_sms()).total : 0; }
+
+spffn_status spffn_kv4_create(const spffn_kv4_config* cfg, void* pool, size_t pool_bytes, const double* rope_freqs,
+                              void* workspace, size_t workspace_bytes, spffn_kv4_ctx** out) {
+    if (!out) return SPFFN_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!valid(cfg) || !pool || !aligned_to(pool, 256) || pool_bytes < spffn_kv4_pool_bytes(cfg)) return SPFFN_ERR_INVALID_ARG;
+    if (cfg->rope_dim && (!rope_freqs || !aligned_to(rope_freqs, 8))) return SPFFN_ERR_INVALID_ARG;
+    const kv4::Layout lay = layout(*cfg, current_sms());
+    if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < lay.total) return SPFFN_ERR_WORKSPACE;
+    spffn_kv4_ctx* c = new (std::nothrow) spffn_kv4_ctx();
+    if (!c) return SPFFN_ERR_UNSUPPORTED;
+    c->cfg = *cfg;
+    c->pool = static_cast<uint8_t*>(pool);
+    c->freqs = rope_freqs;
+    c->ws = static_cast<char*>(workspace);
+    c->lay = lay;
+    c->device = 0;
+    cudaGetDevice(&c->device);
+    cudaGetLastError();
+    c->sms = current_sms();
+    *out = c;
+    return SPFFN_OK;
+}
+
+spffn_status spffn_kv4_destroy(spffn_kv4_ctx* ctx) {
+    delete ctx;
+    return SPFFN_OK;
+}
+
+spffn_status spffn_kv4_append(spffn_kv4_ctx* ctx, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                              int64_t ldv, int32_t T, const int32_t* table, int64_t ld_table, int32_t width,
+                              const int32_t* lens, const int32_t* q_start, int32_t B, void* q_out, int64_t ldqo,
+                              void* stream) {
+    if (!ctx || !valid_batch(ctx, T, table, ld_table, width, lens, q_start, B)) return SPFFN_ERR_INVALID_ARG;
+    if (T == 0 || B == 0) return SPFFN_OK;
+    const auto& c = ctx->cfg;
+    const int64_t qw = (int64_t)c.nh * c.dh, kw = (int64_t)c.kvh * c.dh;
+    if (!k || !v || (!q != !q_out) || ldk < kw || ldv < kw || (q && (ldq < qw || ldqo < qw))) return SPFFN_ERR_INVALID_ARG;
+    if (!aligned_to(q, 2) || !aligned_to(k, 2) || !aligned_to(v, 2) || !aligned_to(q_out, 2)) return SPFFN_ERR_INVALID_ARG;
+    if (q && q == q_out && ldq != ldqo) return SPFFN_ERR_INVALID_ARG;
+    if (!on_device(ctx->device)) return SPFFN_ERR_INVALID_ARG;
+    AppendParams p{q, k, v, q_out, ldq, ldk, ldv, ldqo, ctx->pool, ctx->freqs, c.rope_amplitude, c.nh, c.kvh, c.dh,
+                   c.rope_dim, c.rope_interleaved != 0, batch_of(ctx, T, table, ld_table, width, lens, q_start, B)};
+    const int items = ((q ? c.nh : 0) + 2 * c.kvh) * (c.dh / 8);
+    const dim3 grid(T, std::max(1, std::min(65535, (items + 1023) / 1024)));
+    if (c.dtype == SPFFN_BF16) k_append<__nv_bfloat16><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
+    else k_append<__half><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
+    return record_cuda(cudaGetLastError());
+}
+
+spffn_status spffn_kv4_attend(spffn_kv4_ctx* ctx, const void* q, int64_t ldq, int32_t T, const int32_t* table,
+                              int64_t ld_table, int32_t width, const int32_t* lens, const int32_t* q_start, int32_t B,
+                              float scale, void* out, int64_t ldo, void* stream) {
+    if (!ctx || !valid_batch(ctx, T, table, ld_table, width, lens, q_start, B)) return SPFFN_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return SPFFN_ERR_INVALID_ARG;
+    if (T == 0 || B == 0) return SPFFN_OK;
+    const int64_t qw = (int64_t)ctx->cfg.nh * ctx->cfg.dh;
+    if (!q || !out || q == out || ldq < qw || ldo < qw || !aligned_to(q, 2) || !aligned_to(out, 2)) return SPFFN_ERR_INVALID_ARG;
+    if (!on_device(ctx->device)) return SPFFN_ERR_INVALID_ARG;
+    const AttendArgs a{q, out, ldq, ldo, scale, batch_of(ctx, T, table, ld_table, width, lens, q_start, B)};
+    return record_cuda(launch_attend(*ctx, a, (cudaStream_t)stream));
+}
+
+spffn_status spffn_kv4_read(spffn_kv4_ctx* ctx, const int32_t* page_ids, int32_t n, void* K, void* V, void* stream) {
+    if (!ctx || n < 0) return SPFFN_ERR_INVALID_ARG;
+    if (n == 0) return SPFFN_OK;
+    if (!page_ids || !K || !V || K == V || !aligned_to(page_ids, 4) || !aligned_to(K, 16) || !aligned_to(V, 16)) return SPFFN_ERR_INVALID_ARG;
+    if (!on_device(ctx->device)) return SPFFN_ERR_INVALID_ARG;
+    const auto& c = ctx->cfg;
+    const int64_t items = (int64_t)n * c.page_size * c.kvh * (c.dh / 8);
+    if ((items + 255) / 256 > 0x7fffffffLL) return SPFFN_ERR_INVALID_ARG;
+    const unsigned grid = (unsigned)((items + 255) / 256);
+    cudaStream_t st = (cudaStream_t)stream;
+    auto go = [&](auto tag, auto ng) {
+        using T = decltype(tag);
+        k_read<T, decltype(ng)::value><<<grid, 256, 0, st>>>(ctx->pool, page_ids, items, c.kvh, c.page_size, c.pages,
+                                                             static_cast<T*>(K), static_cast<T*>(V), ctx->err());
+    };
+    auto by_ng = [&](auto tag) {
+        if (c.dh == 64) go(tag, std::integral_constant<int, 2>());
+        else if (c.dh == 128) go(tag, std::integral_constant<int, 4>());
+        else go(tag, std::integral_constant<int, 8>());
+    };
+    if (c.dtype == SPFFN_BF16) by_ng(__nv_bfloat16());
+    else by_ng(__half());
+    return record_cuda(cudaGetLastError());
+}
+
+spffn_status spffn_kv4_last_device_error(spffn_kv4_ctx* ctx, uint32_t* code, void* stream) {
+    if (!ctx) return SPFFN_ERR_INVALID_ARG;
+    return take_device_error(ctx->err(), code, stream);
+}
+
+}  // extern "C"
