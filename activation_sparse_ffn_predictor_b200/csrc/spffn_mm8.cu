@@ -2,52 +2,286 @@
 //   y[t][n] = round( a_scale[t] w_scale[n] sum_k A[t][k] W[n][k] + bias[n] )
 // The 32-bit integer sum is exact (K <= 131072 products of at most 2^14), so any split of K gives
 // the same bits.
+//
+// k_mm8: persistent tcgen05 kernel, int8 x int8 into int32 in TMEM.  A tile is 128 channels (the
+// MMA's M: lane = channel) x BN tokens (its N, any multiple of 16 up to 256), K in blocks of 128
+// bytes: W and A arrive as 2-D TMA tiles of 128-byte rows, 128-byte swizzle, in a ring as deep as
+// shared memory allows.  Channels are M at every batch size, so a decode call streams each weight
+// once with only its tokens' columns as padding (16), and the output's 32-lane rows are whole sectors.
+// Tiles are dealt whole while full waves of CTAs last; the rest (at most two waves) is one line of
+// K blocks cut into equal shares, so every SM streams the same bytes.  A cut tile's CTAs leave their
+// int32 partials in the workspace and count themselves in; the last to arrive adds them: integer sums,
+// so the order does not matter, and nobody waits.
 #include <new>
-#include "spffn_internal.cuh"
+#include "spffn_umma.cuh"
 #include "../../include/spffn_block.h"
 
 namespace spffn {
 namespace {
 
+using namespace um;
+
+constexpr int kTM = 128, kBK = 128, kThreads = 192, kMaxSt = 12;
+constexpr int kGroupN = 8;            // channel tiles that share a stretch of the tile order
+constexpr int kMinBlocks = 4;         // K blocks of a share, at least
+constexpr size_t kSmem = 227 * 1024;
+
 struct MParams {
-    const int8_t *A, *W;
+    CUtensorMap mW, mA;
     const float *a_scale, *w_scale;
     const void* bias;
     void* y;
-    int64_t lda, ldy;
-    int T, K, N;
+    int64_t ldy;
+    int T, N;
+    int kblocks, n_tiles, t_tiles, bn, stages;
+    int whole;                        // tiles per CTA that are dealt whole
+    int cut_base, cut_tiles;          // the tiles that are cut, in line
+    int* partial;                     // [2 grid][bn][128]
+    uint32_t *tickets, *err;
 };
 
-// 64 channels x 64 tokens a CTA, 16 K-words at a time in shared memory, 4 x 4 sums a thread.
-template <typename D>
-__global__ void __launch_bounds__(256) k_mm8_plain(const MParams p) {
-    __shared__ int wa[16][65], ta[16][65];
-    const int n0 = blockIdx.x * 64, t0 = blockIdx.y * 64;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    int acc[4][4] = {};
-    for (int k0 = 0; k0 < p.K; k0 += 64) {
-        for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-            const int r = i >> 4, c = i & 15, k = k0 + 4 * c;
-            wa[c][r] = n0 + r < p.N && k < p.K ? *reinterpret_cast<const int*>(p.W + (int64_t)(n0 + r) * p.K + k) : 0;
-            ta[c][r] = t0 + r < p.T && k < p.K ? *reinterpret_cast<const int*>(p.A + (t0 + r) * p.lda + k) : 0;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(wa[c][tx + 16 * j], ta[c][ty + 16 * i], acc[i][j]);
-        __syncthreads();
+// The pieces of work of one CTA: whole tiles first, then its share of the line.
+struct Walk {
+    int w = 0;
+    long long pos, end;
+    int tile, k0, k1, cut;            // cut: index of the tile in the line, -1 for a whole one
+    __device__ __forceinline__ explicit Walk(const MParams& p) {
+        const long long total = (long long)p.cut_tiles * p.kblocks;
+        pos = total * blockIdx.x / gridDim.x;
+        end = total * (blockIdx.x + 1) / gridDim.x;
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int t = t0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (t >= p.T || n >= p.N) continue;
-            float v = (float)acc[i][j] * (p.a_scale[t] * p.w_scale[n]);
-            if (p.bias) v += DT<D>::f(static_cast<const D*>(p.bias)[n]);
-            static_cast<D*>(p.y)[t * p.ldy + n] = DT<D>::r(v);
+    __device__ __forceinline__ bool next(const MParams& p) {
+        if (w < p.whole) {
+            tile = w++ * gridDim.x + blockIdx.x;
+            k0 = 0;
+            k1 = p.kblocks;
+            cut = -1;
+            return true;
         }
+        if (pos >= end) return false;
+        cut = (int)(pos / p.kblocks);
+        tile = p.cut_base + cut;
+        k0 = (int)(pos - (long long)cut * p.kblocks);
+        k1 = (int)min((long long)p.kblocks, k0 + (end - pos));
+        pos += k1 - k0;
+        if (k0 == 0 && k1 == p.kblocks) cut = -1;
+        return true;
+    }
+};
+
+__device__ __forceinline__ void tile_at(const MParams& p, int tile, int& nt, int& tt) {
+    const int per = kGroupN * p.t_tiles, g = tile / per, r = tile % per;
+    const int gn = min(kGroupN, p.n_tiles - g * kGroupN);
+    nt = g * kGroupN + r % gn;
+    tt = r / gn;
+}
+
+__device__ __forceinline__ void umma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accum), "r"(0u), "r"(0u), "r"(0u), "r"(0u));
+}
+__device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// the four epilogue warps' barrier, and whether all of them say so: they leave a wait together or not at all
+__device__ __forceinline__ bool epi_all(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((uint32_t)ok) : "memory");
+    return r != 0;
+}
+
+template <typename D>
+__global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MParams p) {
+    extern __shared__ __align__(1024) char smem[];
+    char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem) + 1023) & ~uintptr_t(1023));
+    const int S = p.stages, BN = p.bn;
+    const uint32_t stage_bytes = kTM * kBK + BN * kBK;
+    uint64_t* full = reinterpret_cast<uint64_t*>(base + S * stage_bytes);
+    uint64_t* empty = full + kMaxSt;
+    uint64_t* tfull = empty + kMaxSt;      // [2]
+    uint64_t* tempty = tfull + 2;          // [2]
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tempty + 2);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 3);
+    int* s_last = reinterpret_cast<int*>(tempty + 4);
+    uint64_t* done = tempty + 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) { ub_init(&full[i], 1); ub_init(&empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { ub_init(&tfull[i], 1); ub_init(&tempty[i], 4); }
+        ub_init(done, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(tmem_slot)), "r"(512u));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {                   // ------------------------------------ TMA producer
+            int st = 0, ph = 0;
+            uint32_t issued = 0, last_ph = 0;
+            Walk w(p);
+            bool ok = true;
+            while (ok && w.next(p)) {
+                int nt, tt;
+                tile_at(p, w.tile, nt, tt);
+                for (int kb = w.k0; kb < w.k1; ++kb) {
+                    if (!ub_wait(&empty[st], ph ^ 1, abort_flag, p.err)) { ok = false; break; }
+                    char* sw = base + st * stage_bytes;
+                    ub_expect(&full[st], stage_bytes);
+                    tma_2d(sw, &p.mW, kb * kBK, nt * kTM, &full[st]);
+                    tma_2d(sw + kTM * kBK, &p.mA, kb * kBK, tt * BN, &full[st]);
+                    issued |= 1u << st;
+                    last_ph = (last_ph & ~(1u << st)) | ((uint32_t)ph << st);
+                    if (++st == S) { st = 0; ph ^= 1; }
+                }
+            }
+            // a copy that nobody consumed (an abort) has to land before the block ends
+            for (int i = 0; i < S; ++i)
+                if ((issued >> i) & 1u) {
+                    const unsigned long long t0 = now_ns();
+                    while (!ub_try(&full[i], (last_ph >> i) & 1u) && now_ns() - t0 < 20000000ull) {}
+                }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {                   // ------------------------------------ MMA
+            const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kTM >> 4) << 24);
+            int st = 0, ph = 0, ab = 0, aph = 0;
+            Walk w(p);
+            bool ok = true;
+            while (ok && w.next(p)) {
+                if (!ub_wait(&tempty[ab], aph ^ 1, abort_flag, p.err)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(ab * 256);
+                for (int kb = w.k0; kb < w.k1; ++kb) {
+                    if (!ub_wait(&full[st], ph, abort_flag, p.err)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sw = s32(base + st * stage_bytes), sa = sw + kTM * kBK;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_i8(d, sdesc(sw + k * 32u, 1u, 64u), sdesc(sa + k * 32u, 1u, 64u), idesc, kb > w.k0 || k > 0);
+                    ucommit(&empty[st]);
+                    if (++st == S) { st = 0; ph ^= 1; }
+                }
+                if (!ok) break;
+                ucommit(&tfull[ab]);
+                if (++ab == 2) { ab = 0; aph ^= 1; }
+            }
+            if (*abort_flag) {             // what was issued ends before the block does
+                ucommit(done);
+                const unsigned long long t0 = now_ns();
+                while (!ub_try(done, 0) && now_ns() - t0 < 20000000ull) {}
+            }
+        }
+    } else {                               // ---------------------------------------- epilogue
+        const int quad = warp & 3, row = quad * 32 + lane;
+        int ab = 0, aph = 0;
+        Walk w(p);
+        while (w.next(p)) {
+            int nt, tt;
+            tile_at(p, w.tile, nt, tt);
+            const int n = nt * kTM + row;
+            const bool in = n < p.N;
+            const float ws = in ? __ldg(p.w_scale + n) : 0.f;
+            const float bias = in && p.bias ? DT<D>::f(static_cast<const D*>(p.bias)[n]) : 0.f;
+            if (!epi_all(ub_wait(&tfull[ab], aph, abort_flag, p.err))) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(ab * 256);
+            const int t0 = tt * BN, nt_cols = min(BN, p.T - t0);
+            int c_first = 0, c_last = -1;  // the CTAs of a cut tile
+            bool finish = true;
+            if (w.cut >= 0) {
+                const long long total = (long long)p.cut_tiles * p.kblocks, lo = (long long)w.cut * p.kblocks;
+                c_first = (int)(((lo + 1) * gridDim.x - 1) / total);
+                c_last = (int)(((lo + p.kblocks) * gridDim.x - 1) / total);
+                int* mine = p.partial + (size_t)(2 * blockIdx.x + (w.k0 == 0)) * BN * kTM;
+                for (int c0 = 0; c0 < nt_cols; c0 += 16) {
+                    int v[16];
+                    tmem_ld16i(taddr + c0, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) __stcg(mine + (c0 + c) * kTM + row, v[c]);
+                }
+                epi_sync();
+                if (threadIdx.x == 64) {
+                    const uint32_t n_of = (uint32_t)(c_last - c_first + 1);
+                    const uint32_t old = atom_acq_rel_add_u32(&p.tickets[w.cut], 1u);
+                    if (old == n_of - 1) p.tickets[w.cut] = 0;      // for the next call
+                    *s_last = old == n_of - 1;
+                }
+                epi_sync();
+                finish = *s_last;
+            }
+            if (finish) {
+                D* y = static_cast<D*>(p.y) + (int64_t)t0 * p.ldy + n;
+                for (int c0 = 0; c0 < nt_cols; c0 += 16) {
+                    int v[16];
+                    tmem_ld16i(taddr + c0, v);
+                    tmem_wait_ld();
+                    for (int o = c_first; o <= c_last; ++o) {
+                        if (o == (int)blockIdx.x) continue;
+                        // its piece of this tile starts at 0 only if it is the first
+                        const int* from = p.partial + ((size_t)(2 * o + (o == c_first ? 1 : 0)) * BN + c0) * kTM + row;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) v[c] += __ldcg(from + c * kTM);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        if (in && c0 + c < nt_cols)
+                            y[(int64_t)(c0 + c) * p.ldy] = DT<D>::r((float)v[c] * (__ldg(p.a_scale + t0 + c0 + c) * ws) + bias);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ub_arrive(&tempty[ab]);
+            if (++ab == 2) { ab = 0; aph ^= 1; }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+// [rows][cols] bytes of row stride `ld`, box {128, box_rows}, 128-byte swizzle
+bool map_i8(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    EncodeTiledFn enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
+    cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)box_rows}, estr[2] = {1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Layout8 {
+    size_t tickets, partial, total;
+};
+Layout8 layout8(const spffn_mm8_config& c, int sms) {
+    Layout8 l;
+    l.tickets = kCtlBytes;
+    l.partial = align_up(l.tickets + (size_t)2 * sms * sizeof(uint32_t), 256);
+    l.total = l.partial + (size_t)2 * sms * std::min(256, round16(c.max_tokens)) * kTM * sizeof(int);
+    return l;
 }
 
 bool valid(const spffn_mm8_config* c) {
@@ -62,6 +296,7 @@ struct spffn_mm8_ctx {
     spffn_mm8_config cfg;
     spffn_mm8_weights w;
     char* ws;
+    spffn::Layout8 lay;
     int device, sms;
 };
 
@@ -69,7 +304,7 @@ using namespace spffn;
 
 extern "C" {
 
-size_t spffn_mm8_workspace_bytes(const spffn_mm8_config* cfg) { return valid(cfg) ? kCtlBytes : 0; }
+size_t spffn_mm8_workspace_bytes(const spffn_mm8_config* cfg) { return valid(cfg) ? layout8(*cfg, current_sms()).total : 0; }
 
 spffn_status spffn_mm8_create(const spffn_mm8_config* cfg, const spffn_mm8_weights* w, void* workspace,
                               size_t workspace_bytes, spffn_mm8_ctx** out) {
@@ -88,6 +323,7 @@ spffn_status spffn_mm8_create(const spffn_mm8_config* cfg, const spffn_mm8_weigh
     cudaGetDevice(&c->device);
     cudaGetLastError();
     c->sms = current_sms();
+    c->lay = layout8(*cfg, c->sms);
     *out = c;
     return SPFFN_OK;
 }
@@ -104,16 +340,47 @@ spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda,
     if (!A || !a_scale || !y || lda < ctx->cfg.K || ldy < ctx->cfg.N || lda % 16) return SPFFN_ERR_INVALID_ARG;
     if (!aligned_to(A, 16) || !aligned_to(a_scale, 4) || !aligned_to(y, 2)) return SPFFN_ERR_INVALID_ARG;
     if (!on_device(ctx->device)) return SPFFN_ERR_INVALID_ARG;
-    const MParams p{A, ctx->w.W, a_scale, ctx->w.w_scale, ctx->w.bias, y, lda, ldy, T, ctx->cfg.K, ctx->cfg.N};
-    const dim3 grid((p.N + 63) / 64, (T + 63) / 64);
-    if (ctx->cfg.dtype == SPFFN_BF16) k_mm8_plain<__nv_bfloat16><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
-    else k_mm8_plain<__half><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
+    MParams p;
+    const auto& c = ctx->cfg;
+    p.a_scale = a_scale;
+    p.w_scale = ctx->w.w_scale;
+    p.bias = ctx->w.bias;
+    p.y = y;
+    p.ldy = ldy;
+    p.T = T;
+    p.N = c.N;
+    p.kblocks = (c.K + kBK - 1) / kBK;
+    p.n_tiles = (c.N + kTM - 1) / kTM;
+    p.t_tiles = (T + 255) / 256;
+    p.bn = round16((T + p.t_tiles - 1) / p.t_tiles);
+    const size_t stage = (size_t)(kTM + p.bn) * kBK, extra = 1024 + (2 * kMaxSt + 8) * 8;
+    p.stages = (int)std::min<size_t>(kMaxSt, (kSmem - extra) / stage);
+    // whole tiles while two full waves are left, the rest in equal shares
+    const long long tiles = (long long)p.n_tiles * p.t_tiles, total = tiles * p.kblocks;
+    const int grid = (int)std::min<long long>(ctx->sms, std::max<long long>(tiles, total / kMinBlocks));
+    p.whole = tiles % grid == 0 ? (int)(tiles / grid) : (int)std::max<long long>(0, tiles / grid - 1);
+    p.cut_base = p.whole * grid;
+    p.cut_tiles = (int)(tiles - p.cut_base);
+    p.partial = reinterpret_cast<int*>(ctx->ws + ctx->lay.partial);
+    p.tickets = reinterpret_cast<uint32_t*>(ctx->ws + ctx->lay.tickets);
+    p.err = reinterpret_cast<uint32_t*>(ctx->ws);
+    if (!map_i8(&p.mW, ctx->w.W, c.N, c.K, c.K, kTM) || !map_i8(&p.mA, A, T, c.K, lda, p.bn)) return SPFFN_ERR_UNSUPPORTED;
+    const size_t smem = p.stages * stage + extra;
+    auto kern = c.dtype == SPFFN_BF16 ? k_mm8<__nv_bfloat16> : k_mm8<__half>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return record_cuda(e);
+    kern<<<grid, kThreads, smem, (cudaStream_t)stream>>>(p);
     return record_cuda(cudaGetLastError());
 }
 
 spffn_status spffn_mm8_last_device_error(spffn_mm8_ctx* ctx, uint32_t* code, void* stream) {
     if (!ctx) return SPFFN_ERR_INVALID_ARG;
-    return take_device_error(reinterpret_cast<uint32_t*>(ctx->ws), code, stream);
+    const spffn_status s = take_device_error(reinterpret_cast<uint32_t*>(ctx->ws), code, stream);
+    // a call that gave up may have left tiles counted in part
+    if (s == SPFFN_ERR_TIMEOUT &&
+        cudaMemsetAsync(ctx->ws + ctx->lay.tickets, 0, ctx->lay.partial - ctx->lay.tickets, (cudaStream_t)stream) != cudaSuccess)
+        return SPFFN_ERR_CUDA;
+    return s;
 }
 
 }  // extern "C"
