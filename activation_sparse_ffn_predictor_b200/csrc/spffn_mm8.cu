@@ -21,7 +21,8 @@ namespace {
 
 using namespace um;
 
-constexpr int kTM = 128, kBK = 128, kThreads = 192, kMaxSt = 12;
+constexpr int kTM = 128, kBK = 128, kThreads = 320, kMaxSt = 12;
+constexpr int kEpiThreads = 256;      // eight epilogue warps: two for each 32 lanes of TMEM, half the columns each
 constexpr int kGroupN = 8;            // channel tiles that share a stretch of the tile order
 constexpr int kMinBlocks = 4;         // K blocks of a share, at least
 constexpr size_t kSmem = 227 * 1024;
@@ -36,19 +37,23 @@ struct MParams {
     int kblocks, n_tiles, t_tiles, bn, stages;
     int whole;                        // tiles per CTA that are dealt whole
     int cut_base, cut_tiles;          // the tiles that are cut, in line
-    int* partial;                     // [2 grid][bn][128]
+    int4* partial;                    // [2 grid][bn / 4][128 rows] of 4 columns
     uint32_t *tickets, *err;
 };
 
-// The pieces of work of one CTA: whole tiles first, then its share of the line.
+// The pieces of work of one CTA: whole tiles first, then its share of the line, the share's last tile
+// before its first: the front part of a cut tile is then in the workspace long before the CTA with the
+// tile's end looks for it.
 struct Walk {
-    int w = 0;
     long long pos, end;
+    int w = 0, cur, stop;             // tiles of the line still to come, from the last to the first
     int tile, k0, k1, cut;            // cut: index of the tile in the line, -1 for a whole one
     __device__ __forceinline__ explicit Walk(const MParams& p) {
         const long long total = (long long)p.cut_tiles * p.kblocks;
         pos = total * blockIdx.x / gridDim.x;
         end = total * (blockIdx.x + 1) / gridDim.x;
+        cur = pos < end ? (int)((end - 1) / p.kblocks) : -1;
+        stop = pos < end ? (int)(pos / p.kblocks) : 0;
     }
     __device__ __forceinline__ bool next(const MParams& p) {
         if (w < p.whole) {
@@ -58,12 +63,12 @@ struct Walk {
             cut = -1;
             return true;
         }
-        if (pos >= end) return false;
-        cut = (int)(pos / p.kblocks);
+        if (cur < stop) return false;
+        cut = cur--;
         tile = p.cut_base + cut;
-        k0 = (int)(pos - (long long)cut * p.kblocks);
-        k1 = (int)min((long long)p.kblocks, k0 + (end - pos));
-        pos += k1 - k0;
+        const long long lo = (long long)cut * p.kblocks;
+        k0 = (int)max(0ll, pos - lo);
+        k1 = (int)min((long long)p.kblocks, end - lo);
         if (k0 == 0 && k1 == p.kblocks) cut = -1;
         return true;
     }
@@ -91,13 +96,13 @@ __device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int* r) {
         : "r"(taddr));
 }
 
-// the four epilogue warps' barrier, and whether all of them say so: they leave a wait together or not at all
+// the epilogue warps' barrier, and whether all of them say so: they leave a wait together or not at all
 __device__ __forceinline__ bool epi_all(bool ok) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 2, 128, p;\n\t"
+        "barrier.cta.red.and.pred q, 2, 256, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((uint32_t)ok) : "memory");
     return r != 0;
 }
@@ -120,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) { ub_init(&full[i], 1); ub_init(&empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { ub_init(&tfull[i], 1); ub_init(&tempty[i], 4); }
+        for (int i = 0; i < 2; ++i) { ub_init(&tfull[i], 1); ub_init(&tempty[i], kEpiThreads / 32); }
         ub_init(done, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -133,6 +138,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // programmatic dependent launch: what comes before overlaps the previous kernel's end
+    pdl_trigger();
+    pdl_wait();
 
     if (warp == 0) {
         if (lane == 0) {                   // ------------------------------------ TMA producer
@@ -192,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
             }
         }
     } else {                               // ---------------------------------------- epilogue
-        const int quad = warp & 3, row = quad * 32 + lane;
+        const int quad = warp & 3, row = quad * 32 + lane, side = (warp - 2) >> 2;
         int ab = 0, aph = 0;
         Walk w(p);
         while (w.next(p)) {
@@ -202,51 +210,87 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
             const bool in = n < p.N;
             const float ws = in ? __ldg(p.w_scale + n) : 0.f;
             const float bias = in && p.bias ? DT<D>::f(static_cast<const D*>(p.bias)[n]) : 0.f;
-            if (!epi_all(ub_wait(&tfull[ab], aph, abort_flag, p.err))) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(ab * 256);
-            const int t0 = tt * BN, nt_cols = min(BN, p.T - t0);
+            const int t0 = tt * BN, cols = min(BN, p.T - t0);
+            // pieces of 16 columns, the two warps of a quadrant take turns; lane c holds the scale of
+            // the c-th of the 32 columns that the warp finishes at a time
+            float as[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int col = 16 * side + 64 * i + (lane & 15) + 2 * (lane & 16);
+                as[i] = col < cols ? __ldg(p.a_scale + t0 + col) : 0.f;
+            }
             int c_first = 0, c_last = -1;  // the CTAs of a cut tile
+            uint32_t others = 0;           // how many there are beside this one
             bool finish = true;
             if (w.cut >= 0) {
                 const long long total = (long long)p.cut_tiles * p.kblocks, lo = (long long)w.cut * p.kblocks;
                 c_first = (int)(((lo + 1) * gridDim.x - 1) / total);
                 c_last = (int)(((lo + p.kblocks) * gridDim.x - 1) / total);
-                int* mine = p.partial + (size_t)(2 * blockIdx.x + (w.k0 == 0)) * BN * kTM;
-                for (int c0 = 0; c0 < nt_cols; c0 += 16) {
-                    int v[16];
-                    tmem_ld16i(taddr + c0, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) __stcg(mine + (c0 + c) * kTM + row, v[c]);
-                }
-                epi_sync();
-                if (threadIdx.x == 64) {
-                    const uint32_t n_of = (uint32_t)(c_last - c_first + 1);
-                    const uint32_t old = atom_acq_rel_add_u32(&p.tickets[w.cut], 1u);
-                    if (old == n_of - 1) p.tickets[w.cut] = 0;      // for the next call
-                    *s_last = old == n_of - 1;
-                }
-                epi_sync();
+                others = (uint32_t)(c_last - c_first);
+            }
+            if (!epi_all(ub_wait(&tfull[ab], aph, abort_flag, p.err))) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(ab * 256);
+            if (w.cut >= 0) {
+                // where all the others are in, this one's part need not leave TMEM
+                if (threadIdx.x == 64) *s_last = ld_acquire_u32(&p.tickets[w.cut]) == others;
+                epi_all(true);
                 finish = *s_last;
+                if (!finish) {
+                    int4* mine = p.partial + (size_t)(2 * blockIdx.x + (w.k0 == 0)) * (BN / 4) * kTM + row;
+                    for (int c0 = 16 * side; c0 < cols; c0 += 32) {
+                        int v[16];
+                        tmem_ld16i(taddr + c0, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            __stcg(mine + (c0 / 4 + c) * kTM, make_int4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
+                    }
+                    epi_all(true);
+                    if (threadIdx.x == 64) *s_last = atom_acq_rel_add_u32(&p.tickets[w.cut], 1u) == others;
+                    epi_all(true);
+                    finish = *s_last;
+                }
+                if (finish && threadIdx.x == 64) p.tickets[w.cut] = 0;      // for the next call
             }
             if (finish) {
                 D* y = static_cast<D*>(p.y) + (int64_t)t0 * p.ldy + n;
-                for (int c0 = 0; c0 < nt_cols; c0 += 16) {
-                    int v[16];
+                // two pieces at a time, so that a cut tile's partials come 8 loads deep
+                for (int c0 = 16 * side; c0 < cols; c0 += 64) {
+                    int v[32];
+                    const bool two = c0 + 32 < cols;
                     tmem_ld16i(taddr + c0, v);
+                    if (two) tmem_ld16i(taddr + c0 + 32, v + 16);
                     tmem_wait_ld();
+#pragma unroll 2
                     for (int o = c_first; o <= c_last; ++o) {
                         if (o == (int)blockIdx.x) continue;
                         // its piece of this tile starts at 0 only if it is the first
-                        const int* from = p.partial + ((size_t)(2 * o + (o == c_first ? 1 : 0)) * BN + c0) * kTM + row;
+                        const int4* from = p.partial + ((size_t)(2 * o + (o == c_first ? 1 : 0)) * (BN / 4) + c0 / 4) * kTM + row;
+                        int4 u[8];
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) v[c] += __ldcg(from + c * kTM);
+                        for (int c = 0; c < 4; ++c) {
+                            u[c] = __ldcg(from + c * kTM);
+                            u[c + 4] = two ? __ldcg(from + (c + 8) * kTM) : make_int4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            v[4 * c] += u[c].x;
+                            v[4 * c + 1] += u[c].y;
+                            v[4 * c + 2] += u[c].z;
+                            v[4 * c + 3] += u[c].w;
+                        }
                     }
+                    const float asc = as[0];
+                    as[0] = as[1];
+                    as[1] = as[2];
+                    as[2] = as[3];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        if (in && c0 + c < nt_cols)
-                            y[(int64_t)(c0 + c) * p.ldy] = DT<D>::r((float)v[c] * (__ldg(p.a_scale + t0 + c0 + c) * ws) + bias);
+                    for (int c = 0; c < 32; ++c) {
+                        const int col = c0 + (c & 15) + 2 * (c & 16);
+                        const float f = __shfl_sync(0xffffffffu, asc, c) * ws;
+                        if (in && col < cols) y[(int64_t)col * p.ldy] = DT<D>::r((float)v[c] * f + bias);
+                    }
                 }
             }
             tc_fence_before();
@@ -361,7 +405,7 @@ spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda,
     p.whole = tiles % grid == 0 ? (int)(tiles / grid) : (int)std::max<long long>(0, tiles / grid - 1);
     p.cut_base = p.whole * grid;
     p.cut_tiles = (int)(tiles - p.cut_base);
-    p.partial = reinterpret_cast<int*>(ctx->ws + ctx->lay.partial);
+    p.partial = reinterpret_cast<int4*>(ctx->ws + ctx->lay.partial);
     p.tickets = reinterpret_cast<uint32_t*>(ctx->ws + ctx->lay.tickets);
     p.err = reinterpret_cast<uint32_t*>(ctx->ws);
     if (!map_i8(&p.mW, ctx->w.W, c.N, c.K, c.K, kTM) || !map_i8(&p.mA, A, T, c.K, lda, p.bn)) return SPFFN_ERR_UNSUPPORTED;
@@ -369,8 +413,17 @@ spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda,
     auto kern = c.dtype == SPFFN_BF16 ? k_mm8<__nv_bfloat16> : k_mm8<__half>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return record_cuda(e);
-    kern<<<grid, kThreads, smem, (cudaStream_t)stream>>>(p);
-    return record_cuda(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return record_cuda(cudaLaunchKernelEx(&cfg, kern, p));
 }
 
 spffn_status spffn_mm8_last_device_error(spffn_mm8_ctx* ctx, uint32_t* code, void* stream) {
