@@ -1,93 +1,845 @@
-// Attention over the paged 4-bit cache (spffn_kv4_attend in include/spffn_block.h).
+// Attention over the paged 4-bit cache (spffn_kv4_attend in include/spffn_block.h):
+//   out = sum_j softmax_j(scale q . K_j) V_j,   K_j = code step + zero per group of 32 dims
+//
+// Mathematics.  With n the codes, s the steps and z the zeros of a position j and a group g,
+//   q . K_j = sum_g s_jg (q_g . n_jg) + sum_g z_jg (sum of q_g)
+//   sum_j p_j V_j = sum_j (p_j s_jg) n_jg + sum_j p_j z_jg
+// so the codes enter the matrix instructions as they are and steps and zeros touch only scores and
+// probabilities: 16 positions x 8 query rows instead of 16 positions x dh values.
+//
+// Matrix instructions: mma.m16n8k16 in fp16 with fp32 sums.  Positions (for scores) and dims (for
+// the output) are the 16 rows, query rows the 8 columns, so a head group of up to 8 rows costs one
+// instruction per 16 x 16 codes and no row of it is padding for long contexts.  A code n in the low
+// bits of a halfword is the fp16 subnormal n 2^-24 and in bits 4..7 n 2^-20: two ANDs turn a word
+// into operands, no conversion; the 2^-24 and the 16 are undone on scores, outputs and q.
+// q is brought to [2^9, 2^10) by a power of two per row (exact), so a bf16 q fits fp16; the sums of
+// q_g enter as a high and a low half.  Probabilities are rounded to fp16 once alone and once times
+// the step (2^-11 each, against 2^-9 or 2^-12 of the output's own rounding); they are kept as
+// 2^(15 - R) p, R the largest exponent of a V step seen, so that p s stays in fp16's normal range.
+//
+// Work: a unit is 32 positions of one (sequence, kv head, tile of query rows).  The units of the
+// batch are one line, cut into equal shares, one a block; blocks find their share from the lengths
+// on the device (a captured graph replays with other lengths).  In a block the units go round the
+// warps; each warp streams its own through a ring of bulk copies (a unit is one stretch of a page,
+// two where pages have 16 tokens) and nothing waits for another warp until a head's end, where
+// the warps' states are joined through shared memory.  A head that several blocks share leaves
+// its states in the workspace; the last block to arrive joins them in their order, so the result
+// does not depend on which it is.
+#include "spffn_umma.cuh"
 #include "spffn_kv4.cuh"
 
 namespace spffn {
 namespace kv4 {
 namespace {
 
+using um::now_ns;
+using um::s32;
+using um::ub_expect;
+using um::ub_init;
+using um::ub_try;
+
+constexpr int kUnit = 32;             // positions of a unit
+constexpr float kLog2e = 1.4426950408889634f;
+
 struct KParams {
     AttendArgs a;
     const uint8_t* pool;
-    int nh, kvh;
+    float* part;                      // [2 grid][slot floats]
+    uint32_t* tickets;                // [grid]
+    int nh, kvh, G;
+    int qvec, ovec;                   // rows of q in 16-byte pieces, rows of out in 8-byte pieces
 };
 
-// One warp per (row, query head): one pass over the row's positions with the running maximum and sum.
-// Lane l holds dims l, l + 32, ...
-template <typename T, int NG>
-__global__ void __launch_bounds__(128) k_attend_plain(const KParams p) {
+__device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {     // a in the low half
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ uint32_t as_u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(s32(bar)) : "memory");
+}
+// N words of shared memory
+template <int N> __device__ __forceinline__ void lds(uint32_t* w, const uint8_t* p) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x; w[1] = v.y;
+    } else {
+        static_assert(N == 1, "");
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+}
+
+// A place in the line of units: (sequence, kv head, row tile, unit of it).  Pairs that differ in
+// the row tile alone are neighbours, so their positions come from L2 the second time.
+template <int R> struct Place {
+    int b, hk, rt, u;
+    int row0, n, len, ok;             // of the sequence
+    int nrt, units, keys;             // its row tiles; units and visible positions of this row tile
+    __device__ __forceinline__ void load_seq(const KParams& p) {
+        const Seq s = seq_of(p.a.b, b);
+        row0 = s.row0; n = s.n; len = s.len; ok = s.ok;
+        nrt = (n * p.G + R - 1) / R;
+    }
+    static __device__ __forceinline__ int keys_of(int rt, int n, int len, bool ok, int G) {
+        return ok ? len - n + (min((rt + 1) * R, n * G) - 1) / G + 1 : 0;
+    }
+    // a sequence whose length was refused keeps one unit a tile, without positions: its rows become 0
+    static __device__ __forceinline__ int units_of(int keys) { return max(1, (keys + kUnit - 1) / kUnit); }
+    __device__ __forceinline__ void load_tile(const KParams& p) {
+        keys = keys_of(rt, n, len, ok, p.G);
+        units = units_of(keys);
+    }
+    __device__ __forceinline__ void next_pair(const KParams& p) {
+        if (++rt == nrt) {
+            rt = 0;
+            if (++hk == p.kvh) {
+                hk = 0;
+                do {
+                    ++b;
+                    if (b >= p.a.b.B) return;
+                    load_seq(p);
+                } while (n == 0);
+            }
+        }
+        load_tile(p);
+    }
+    __device__ __forceinline__ void advance(const KParams& p, int by) {
+        u += by;
+        while (u >= units) {
+            u -= units;
+            next_pair(p);
+            if (b >= p.a.b.B) return;
+        }
+    }
+};
+
+// The running state of a tile of 8 NT query rows: thread (r, c) = (lane / 4, lane % 4) holds query columns
+// 2c, 2c + 1 of each 8; o[2g + i][.][0, 1] dim 32g + 4r + 2i and [2, 3] dim + 1 of them.  `off`: the
+// exponent that probabilities are taken against, -inf before the first.
+template <int NG, int NT> struct State {
+    float off[NT][2], l[NT][2], o[2 * NG][NT][4];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            off[t][0] = off[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2 * NG; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[j][t][i] = 0.f;
+        }
+    }
+};
+
+template <int NG, int NT, int W> struct Smem {
+    static constexpr int kJoin = (W / 2 > 0 ? W / 2 : 1) * NT * 8 * NG * 32 * 4;   // states of half the warps
+};
+
+template <typename T, int NG, int NT, int W, int NS>
+__global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
     using L = Blk<NG>;
-    const Batch& b = p.a.b;
-    const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    const int t = (int)(w / p.nh), h = (int)(w % p.nh);
-    if (t >= b.T) return;
-    const int s = seq_of_row(b, t);
-    if (s < 0) return;
-    const Seq sq = seq_of(b, s);
-    if (t < sq.row0 || t >= sq.row0 + sq.n) return;
-    const int keys = sq.ok ? sq.len - sq.n + (t - sq.row0) + 1 : 0;
-    const int hk = h / (p.nh / p.kvh);
-    const T* q = static_cast<const T*>(p.a.q) + t * p.a.ldq + (int64_t)h * (32 * NG);
-    float qv[NG], o[NG], m = -INFINITY, sum = 0.f;
+    constexpr int R = 8 * NT, DH = 32 * NG;
+    constexpr uint32_t kTile = 2 * L::kBytes;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* ring = smem;                                         // [W][NS][kTile]
+    float* join = reinterpret_cast<float*>(smem + W * NS * kTile);
+    float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(join) + Smem<NG, NT, W>::kJoin);   // [W][R]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ml + W * R);     // [W][NS]
+    long long* scan = reinterpret_cast<long long*>(bars + W * NS);
+    int* misc = reinterpret_cast<int*>(scan + W + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const Batch& bt = p.a.b;
+
+    // ---------------------------------------------------- this block's share of the line
+    if (threadIdx.x < W * NS) ub_init(&bars[threadIdx.x], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    um::pdl_trigger();
+    um::pdl_wait();
+    const int per = (bt.B + 32 * W - 1) / (32 * W);
+    auto units_of_seq = [&](int s) -> long long {
+        const Seq q = seq_of(bt, s);
+        const int nrt = (q.n * p.G + R - 1) / R;
+        long long sum = 0;
+        for (int t = 0; t < nrt; ++t) sum += Place<R>::units_of(Place<R>::keys_of(t, q.n, q.len, q.ok, p.G));
+        return sum * p.kvh;
+    };
+    long long mine = 0;
+    for (int s = threadIdx.x * per; s < min(bt.B, ((int)threadIdx.x + 1) * per); ++s) mine += units_of_seq(s);
+    long long pref = mine;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        qv[g] = DT<T>::f(q[32 * g + lane]) * p.a.scale;
-        o[g] = 0.f;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, pref, o);
+        if (lane >= o) pref += v;
     }
-    for (int j = 0; j < keys; ++j) {
-        const int page = b.table[s * b.ldt + j / b.page];
-        if (page < 0 || page >= b.pages) {
-            if (lane == 0) latch(b.err, ERR_PAGE_RANGE);
-            continue;
-        }
-        const int tok = j % b.page, lt = tok & 15;
-        const uint8_t* rec = p.pool + (((int64_t)page * p.kvh + hk) * (b.page >> 4) + (tok >> 4)) * L::kBytes;
-        auto half_at = [&](int off) { return __half2float(*reinterpret_cast<const __half*>(rec + off)); };
-        float dot = 0.f;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const int code = (rec[L::k(lt, g, lane >> 3) + ((lane & 7) >> 1)] >> (4 * (lane & 1))) & 15;
-            dot += qv[g] * fmaf((float)code, half_at(L::ks(lt, g)), half_at(L::kz(lt, g)));
-        }
-        dot = warp_sum(dot);
-        const float mn = fmaxf(m, dot), f = m == -INFINITY ? 0.f : __expf(m - mn), pr = __expf(dot - mn);
-        sum = sum * f + pr;
-        m = mn;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const int code = (rec[L::v(lt, g, lane >> 2) + ((lane & 3) >> 1)] >> (4 * (lane & 1))) & 15;
-            o[g] = o[g] * f + pr * fmaf((float)code, half_at(L::vs(lt, g)), half_at(L::vz(lt, g)));
+    if (lane == 31) scan[warp] = pref;
+    __syncthreads();
+    long long total = 0;
+    pref -= mine;
+    for (int w = 0; w < W; ++w) {
+        if (w < warp) pref += scan[w];
+        total += scan[w];
+    }
+    // no more blocks than there are rounds of the warps
+    const long long blocks = min((long long)gridDim.x, max(1ll, total / W));
+    if ((long long)blockIdx.x >= blocks) return;
+    const long long lo = total * blockIdx.x / blocks, hi = total * (blockIdx.x + 1) / blocks;
+    if (lo >= hi) return;
+    if (lo >= pref && lo < pref + mine) {
+        for (int s = threadIdx.x * per;; ++s) {
+            const long long here = units_of_seq(s);
+            if (lo < pref + here) {
+                const Seq q = seq_of(bt, s);
+                const long long of_head = here / p.kvh;
+                long long in = lo - pref;
+                int t = 0;
+                misc[0] = s;
+                misc[1] = (int)(in / of_head);
+                in %= of_head;
+                for (;; ++t) {
+                    const int u = Place<R>::units_of(Place<R>::keys_of(t, q.n, q.len, q.ok, p.G));
+                    if (in < u) break;
+                    in -= u;
+                }
+                misc[2] = t;
+                misc[3] = (int)in;
+                break;
+            }
+            pref += here;
         }
     }
-    T* out = static_cast<T*>(p.a.out) + t * p.a.ldo + (int64_t)h * (32 * NG);
+    __syncthreads();
+    Place<R> at;                                                  // where the block stands
+    at.b = misc[0]; at.hk = misc[1]; at.rt = misc[2]; at.u = misc[3];
+    at.load_seq(p);
+    at.load_tile(p);
+
+    // ------------------------------------------------------------ the warp's ring of copies
+    uint8_t* my_ring = ring + warp * NS * kTile;
+    uint64_t* my_bar = bars + warp * NS;
+    Place<R> ahead = at;                                          // the next unit to ask for
+    long long x_ahead = lo + warp;
+    if (x_ahead < hi) ahead.advance(p, warp);
+    int page0 = -1, page1 = -1;
+    uint32_t valid = 0, phases = 0, issued = 0;                   // 2 bits, 1 bit, 1 bit a stage
+    bool failed = false;
+    auto look_up = [&]() {                                        // the pages of `ahead`, used one round later
+        if (x_ahead >= hi) return;
+        const int pos = ahead.u * kUnit;
+        const int32_t* row = bt.table + ahead.b * bt.ldt;
+        page0 = pos < ahead.keys ? __ldg(row + (pos >> bt.page_log)) : -1;
+        page1 = pos + 16 < ahead.keys ? (bt.page_log == 4 ? __ldg(row + (pos >> 4) + 1) : page0) : -1;
+    };
+    auto ask = [&](int st) {
+        valid &= ~(3u << (2 * st));
+        issued &= ~(1u << st);
+        if (x_ahead >= hi || failed) return;
+        const int pos = ahead.u * kUnit;
+        const bool in0 = (unsigned)page0 < (unsigned)bt.pages, in1 = (unsigned)page1 < (unsigned)bt.pages;
+        if ((pos < ahead.keys && !in0) || (pos + 16 < ahead.keys && !in1)) {
+            if (lane == 0) latch(bt.err, ERR_PAGE_RANGE);
+        }
+        valid |= ((in0 ? 1u : 0u) | (in1 ? 2u : 0u)) << (2 * st);
+        if (in0 || in1) {
+            issued |= 1u << st;
+            if (lane == 0) {
+                const uint32_t dst = s32(my_ring + st * kTile);
+                auto src = [&](int page, int pp) {
+                    return p.pool + (((int64_t)page * p.kvh + ahead.hk) * (bt.page >> 4) + ((pp & (bt.page - 1)) >> 4)) * L::kBytes;
+                };
+                ub_expect(&my_bar[st], (in0 ? L::kBytes : 0) + (in1 ? L::kBytes : 0));
+                if (in0 && in1 && bt.page_log > 4) bulk_copy(dst, src(page0, pos), kTile, &my_bar[st]);
+                else {
+                    if (in0) bulk_copy(dst, src(page0, pos), L::kBytes, &my_bar[st]);
+                    if (in1) bulk_copy(dst + L::kBytes, src(page1, pos + 16), L::kBytes, &my_bar[st]);
+                }
+            }
+        }
+        x_ahead += W;
+        if (x_ahead < hi) ahead.advance(p, W);
+        look_up();
+    };
+    look_up();
 #pragma unroll
-    for (int g = 0; g < NG; ++g) out[32 * g + lane] = DT<T>::r(sum == 0.f ? 0.f : o[g] / sum);
+    for (int i = 0; i < NS; ++i) ask(i);
+
+    // -------------------------------------------------------------------- the block's heads
+    int st = 0;
+    long long x = lo;
+    while (x < hi) {
+        const int u0 = at.u, u1 = (int)min((long long)at.units, u0 + (hi - x));
+        State<NG, NT> s;
+        s.clear();
+        float oz[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) oz[t][i] = 0.f;
+        // q of row r as the second operand, its group sums as halves, the factor of the columns' scores
+        uint32_t qf[NT][NG][4], qs[NT][2];
+        float fq[NT][2], mx[NT][2];
+        int pos[NT][2];
+        int vexp = 0;                                             // R: V steps seen are below 2^R
+        const int rows = at.n * p.G;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int row = at.rt * R + t * 8 + r;
+            float q[8 * NG], big = 0.f, bad = 0.f;
+            if (row < rows) {
+                const T* src = static_cast<const T*>(p.a.q) + (int64_t)(at.row0 + row / p.G) * p.a.ldq +
+                               (int64_t)(at.hk * p.G + row % p.G) * DH + 8 * c;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    if (p.qvec) unpack8<T>(*reinterpret_cast<const uint4*>(src + 32 * g), q + 8 * g);
+                    else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) q[8 * g + i] = DT<T>::f(src[32 * g + i]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8 * NG; ++i) {
+                    big = fmaxf(big, fabsf(q[i]));
+                    bad += q[i] * 0.f;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8 * NG; ++i) q[i] = 0.f;
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                bad += __shfl_xor_sync(0xffffffffu, bad, o);
+            }
+            const int e = (int)(__float_as_uint(big) >> 23) - 127;
+            const int k = big == 0.f ? 0 : min(126, 9 - e);
+            const float up = bad == 0.f ? __uint_as_float((uint32_t)(127 + k) << 23) : __int_as_float(0x7fc00000);
+            const float f = p.a.scale * kLog2e * __uint_as_float((uint32_t)(127 - k) << 23);
+            fq[t][0] = __shfl_sync(0xffffffffu, f, 8 * c);        // of rows 2c and 2c + 1
+            fq[t][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+            uint32_t hs = 0, ls = 0;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                float h[8], sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    h[i] = __half2float(__float2half_rn(q[8 * g + i] * up));
+                    sum += h[i];
+                }
+                // codes 0, 4 | 1, 5 (times 16) | 2, 6 | 3, 7 (times 16) of the word
+                qf[t][g][0] = pack2(h[0], h[4]);
+                qf[t][g][1] = pack2(h[1] * 0.0625f, h[5] * 0.0625f);
+                qf[t][g][2] = pack2(h[2], h[6]);
+                qf[t][g][3] = pack2(h[3] * 0.0625f, h[7] * 0.0625f);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if (g >> 1 == c) {
+                    const __half hi16 = __float2half_rn(sum), lo16 = __float2half_rn(sum - __half2float(hi16));
+                    hs |= (uint32_t)__half_as_ushort(hi16) << (16 * (g & 1));
+                    ls |= (uint32_t)__half_as_ushort(lo16) << (16 * (g & 1));
+                }
+            }
+            qs[t][0] = hs;
+            qs[t][1] = ls;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int rw = at.rt * R + t * 8 + 2 * c + i;
+                pos[t][i] = at.len - at.n + rw / p.G;             // of rows past the last: never written
+                mx[t][i] = -INFINITY;
+            }
+        }
+        const int clear_to = at.len - at.n + at.rt * R / p.G + 1; // positions that every row sees
+
+        // the warp's units of this head
+        const int first = (int)((warp - (x - lo)) % W + W) % W;
+        for (int u = u0 + first; u < u1 && !failed; u += W) {
+            const uint8_t* tile = my_ring + st * kTile;
+            const uint32_t have = (valid >> (2 * st)) & 3u;
+            if ((issued >> st) & 1u) {
+                const uint32_t ph = (phases >> st) & 1u;
+                if (!ub_try(&my_bar[st], ph)) {
+                    const unsigned long long t0 = now_ns();
+                    while (!ub_try(&my_bar[st], ph)) {
+                        if (now_ns() - t0 > um::kUWaitNs) {
+                            failed = true;
+                            break;
+                        }
+                    }
+                }
+                failed = __any_sync(0xffffffffu, failed);
+                phases ^= 1u << st;
+            }
+            if (failed) {
+                if (lane == 0) latch(bt.err, ERR_PIPE_TIMEOUT);
+                break;
+            }
+            const int p0 = u * kUnit;
+            if (have) {
+                // V steps: their largest exponent, and what must not enter the products: positions past
+                // the last and steps that are not numbers (their rows see that in their scores)
+                uint32_t nan_tok = 0;                             // bit t: position p0 + t has such a step
+                __half2 top = __float2half2_rn(0.f);
+                auto tops = [&]() {
+                    top = __float2half2_rn(0.f);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (!((have >> j) & 1u)) continue;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t v[NG];
+                            lds<NG>(v, tile + j * L::kBytes + L::kVs + h * 16 * NG + c * 4 * NG);
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) top = __hmax2_nan(top, as_h2(v[g]));
+                        }
+                    }
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1) top = __hmax2_nan(top, as_h2(__shfl_xor_sync(0xffffffffu, as_u(top), o)));
+                };
+                const bool edge = p0 + kUnit > at.keys;
+                if (!edge) tops();
+                if (edge || __hisnan(__low2half(top)) || __hisnan(__high2half(top))) {
+                    uint8_t* w = const_cast<uint8_t*>(tile);
+                    const int j = lane >> 4, tok = lane & 15;     // a lane a position
+                    if ((have >> j) & 1u) {
+                        bool nan = false;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) nan |= __hisnan(*reinterpret_cast<const __half*>(w + j * L::kBytes + L::vs(tok, g)));
+                        if (nan || p0 + lane >= at.keys) {
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                *reinterpret_cast<uint16_t*>(w + j * L::kBytes + L::vs(tok, g)) = 0;
+                                *reinterpret_cast<uint16_t*>(w + j * L::kBytes + L::vz(tok, g)) = 0;
+                            }
+                            nan_tok = nan ? 1u << lane : 0u;
+                        }
+                    }
+                    um::fence_async_smem();                       // the ring's next copy comes by another proxy
+                    nan_tok = __reduce_or_sync(0xffffffffu, nan_tok);
+                    __syncwarp();
+                    tops();
+                }
+                const float vt = fmaxf(__low2float(top), __high2float(top));
+                const int ve = (int)(__float_as_uint(vt) >> 23) - 126;                          // vt < 2^ve
+                const int vnew = max(vexp, ve);
+
+                // scores of the unit: position r (and r + 8) of each block of 16, columns 2c, 2c + 1
+                float sc[2][NT][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint8_t* blk = tile + j * L::kBytes;
+                    uint32_t w0[NG], w1[NG], st0[(NG + 1) / 2], st1[(NG + 1) / 2];
+                    lds<NG>(w0, blk + r * 16 * NG + c * 4 * NG);
+                    lds<NG>(w1, blk + (r + 8) * 16 * NG + c * 4 * NG);
+                    lds<NG / 2>(st0, blk + L::kKs + r * 2 * NG);
+                    lds<NG / 2>(st1, blk + L::kKs + (r + 8) * 2 * NG);
+                    uint32_t z0 = 0, z1 = 0;
+                    if (2 * c < NG) {
+                        z0 = *reinterpret_cast<const uint32_t*>(blk + L::kKz + r * 2 * NG + 4 * c);
+                        z1 = *reinterpret_cast<const uint32_t*>(blk + L::kKz + (r + 8) * 2 * NG + 4 * c);
+                    }
+                    float part[NT][4];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) part[t][i] = sc[j][t][i] = 0.f;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma(sc[j][t], z0, z1, z0, z1, qs[t][0], qs[t][1]);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const float2 s0 = __half22float2(as_h2(st0[g >> 1])), s1 = __half22float2(as_h2(st1[g >> 1]));
+                        const float k0 = g & 1 ? s0.y : s0.x, k1 = g & 1 ? s1.y : s1.x;
+                        const uint32_t a0 = w0[g] & 0x000f000fu, a2 = w0[g] & 0x00f000f0u, b0 = (w0[g] >> 8) & 0x000f000fu,
+                                       b2 = (w0[g] >> 8) & 0x00f000f0u;
+                        const uint32_t a1 = w1[g] & 0x000f000fu, a3 = w1[g] & 0x00f000f0u, b1 = (w1[g] >> 8) & 0x000f000fu,
+                                       b3 = (w1[g] >> 8) & 0x00f000f0u;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma(d, a0, a1, a2, a3, qf[t][g][0], qf[t][g][1]);
+                            mma(d, b0, b1, b2, b3, qf[t][g][2], qf[t][g][3]);
+                            part[t][0] = fmaf(d[0], k0, part[t][0]);
+                            part[t][1] = fmaf(d[1], k0, part[t][1]);
+                            part[t][2] = fmaf(d[2], k1, part[t][2]);
+                            part[t][3] = fmaf(d[3], k1, part[t][3]);
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sc[j][t][i] = fmaf(part[t][i], 16777216.f, sc[j][t][i]) * fq[t][i & 1];
+                }
+                if (p0 + kUnit > clear_to || have != 3u || nan_tok) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int tok = 16 * j + r + 8 * (i >> 1);
+                                if (p0 + tok > pos[t][i & 1] || p0 + tok >= at.keys || !((have >> j) & 1u)) sc[j][t][i] = -INFINITY;
+                                else if ((nan_tok >> tok) & 1u) sc[j][t][i] = __int_as_float(0x7fc00000);
+                            }
+                }
+                // running maximum, and what it does to the state
+                bool moved = false;
+                float f[NT][2];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float m = fmaxf(fmaxf(sc[0][t][i], sc[0][t][i + 2]), fmaxf(sc[1][t][i], sc[1][t][i + 2]));
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        m = fmaxf(m, mx[t][i]);
+                        mx[t][i] = m;
+                        const float off = m == -INFINITY ? -INFINITY : m + (float)(vnew - 15);
+                        f[t][i] = off == s.off[t][i] ? 1.f : ex2(s.off[t][i] - off);
+                        moved |= f[t][i] != 1.f;
+                        s.off[t][i] = off;
+                    }
+                vexp = vnew;
+                if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            s.l[t][i] *= f[t][i];
+                            oz[t][i] *= f[t][i];
+                            oz[t][i + 2] *= f[t][i];
+#pragma unroll
+                            for (int d = 0; d < 2 * NG; ++d) {
+                                s.o[d][t][i] *= f[t][i];
+                                s.o[d][t][i + 2] *= f[t][i];
+                            }
+                        }
+                }
+                // probabilities, turned into the second operand of the output's product
+                uint32_t pb[2][NT][2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        float pr[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float off = s.off[t][i & 1];
+                            pr[i] = ex2(sc[j][t][i] - (off == -INFINITY ? 0.f : off));
+                            s.l[t][i & 1] += pr[i];
+                        }
+                        pb[j][t][0] = transpose8(pack2(pr[0], pr[1]));
+                        pb[j][t][1] = transpose8(pack2(pr[2], pr[3]));
+                    }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (!((have >> j) & 1u)) continue;
+                    const uint8_t* blk = tile + j * L::kBytes;
+                    uint32_t w0[NG], w1[NG], s0[NG], s1[NG];       // words of tokens 2c, 2c + 1 | 2c + 8, 2c + 9
+                    lds<NG>(w0, blk + L::kV + r * 16 * NG + c * 4 * NG);
+                    lds<NG>(w1, blk + L::kV + 128 * NG + r * 16 * NG + c * 4 * NG);
+                    lds<NG>(s0, blk + L::kVs + c * 4 * NG);
+                    lds<NG>(s1, blk + L::kVs + 16 * NG + c * 4 * NG);
+                    uint32_t z0 = 0, z1 = 0;
+                    if (r < NG) {
+                        z0 = *reinterpret_cast<const uint32_t*>(blk + L::kVz + c * 4 * NG + 4 * r);
+                        z1 = *reinterpret_cast<const uint32_t*>(blk + L::kVz + 16 * NG + c * 4 * NG + 4 * r);
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma(oz[t], z0, 0u, z1, 0u, pb[j][t][0], pb[j][t][1]);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        uint32_t b0[NT], b1[NT];
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            b0[t] = as_u(__hmul2(as_h2(pb[j][t][0]), as_h2(s0[g])));
+                            b1[t] = as_u(__hmul2(as_h2(pb[j][t][1]), as_h2(s1[g])));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            // byte i of group g of the two tokens, one in each half
+                            const int wd = g >> 1, by = 2 * (g & 1) + i;
+                            const uint32_t sel = (uint32_t)(by | (by << 4) | ((4 + by) << 8) | ((4 + by) << 12));
+                            const uint32_t a = __byte_perm(w0[wd], w0[NG / 2 + wd], sel), b = __byte_perm(w1[wd], w1[NG / 2 + wd], sel);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+                                mma(s.o[2 * g + i][t], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, b0[t], b1[t]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();                                         // every lane has read the stage
+            ask(st);
+            st = st + 1 == NS ? 0 : st + 1;
+        }
+
+        // ------------------------------------------------ the warps' states become one
+        // the sums over r of l; codes' and zeros' parts together, in true units
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) s.l[t][i] += __shfl_xor_sync(0xffffffffu, s.l[t][i], o);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const float z = __shfl_sync(0xffffffffu, oz[t][i], 4 * g + c);
+#pragma unroll
+                    for (int d = 2 * g; d < 2 * g + 2; ++d) {
+                        s.o[d][t][i] = fmaf(s.o[d][t][i], 16777216.f, z);
+                        s.o[d][t][i + 2] = fmaf(s.o[d][t][i + 2], 1048576.f, z);
+                    }
+                }
+            }
+        auto join_warps = [&]() {                                 // warp 0 ends up with the sum
+            if (r == 0) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) ml[warp * R + t * 8 + 2 * c + i] = make_float2(s.off[t][i], s.l[t][i]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float m = -INFINITY, l = 0.f;
+                    for (int w = 0; w < W; ++w) m = fmaxf(m, ml[w * R + t * 8 + 2 * c + i].x);
+                    const float base = m == -INFINITY ? 0.f : m;
+                    for (int w = 0; w < W; ++w) {
+                        const float2 v = ml[w * R + t * 8 + 2 * c + i];
+                        l += v.y * ex2(v.x - base);
+                    }
+                    const float f = ex2(s.off[t][i] - base);
+                    s.off[t][i] = m;
+                    s.l[t][i] = l;
+#pragma unroll
+                    for (int d = 0; d < 2 * NG; ++d) {
+                        s.o[d][t][i] *= f;
+                        s.o[d][t][i + 2] *= f;
+                    }
+                }
+#pragma unroll
+            for (int h = W / 2; h >= 1; h >>= 1) {
+                if (warp >= h && warp < 2 * h) {
+                    float* to = join + (size_t)(warp - h) * (NT * 8 * NG * 32) + lane;
+#pragma unroll
+                    for (int d = 0; d < 2 * NG; ++d)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) to[((d * NT + t) * 4 + i) * 32] = s.o[d][t][i];
+                }
+                __syncthreads();
+                if (warp < h) {
+                    const float* from = join + (size_t)warp * (NT * 8 * NG * 32) + lane;
+#pragma unroll
+                    for (int d = 0; d < 2 * NG; ++d)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) s.o[d][t][i] += from[((d * NT + t) * 4 + i) * 32];
+                }
+                if (h > 1) __syncthreads();
+            }
+        };
+        auto write_out = [&]() {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = at.rt * R + t * 8 + 2 * c + i;
+                    if (row >= rows) continue;
+                    T* to = static_cast<T*>(p.a.out) + (int64_t)(at.row0 + row / p.G) * p.a.ldo + (int64_t)(at.hk * p.G + row % p.G) * DH + 4 * r;
+                    const float inv = s.l[t][i] == 0.f ? 0.f : 1.f / s.l[t][i];
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        T v[4] = {DT<T>::r(s.o[2 * g][t][i] * inv), DT<T>::r(s.o[2 * g][t][i + 2] * inv),
+                                  DT<T>::r(s.o[2 * g + 1][t][i] * inv), DT<T>::r(s.o[2 * g + 1][t][i + 2] * inv)};
+                        if (p.ovec) *reinterpret_cast<uint2*>(to + 32 * g) = *reinterpret_cast<const uint2*>(v);
+                        else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) to[32 * g + k] = v[k];
+                        }
+                    }
+                }
+        };
+        join_warps();
+        const long long head_lo = x - u0;                         // the head's stretch of the line
+        const bool whole = u0 == 0 && u1 == at.units;
+        if (whole) {
+            if (warp == 0) write_out();
+        } else {
+            constexpr int kSlot = NT * 8 * NG * 32 + 2 * R;
+            const int c_first = (int)(((head_lo + 1) * blocks - 1) / total), c_last = (int)(((head_lo + at.units) * blocks - 1) / total);
+            if (warp == 0) {
+                float* to = p.part + (size_t)(2 * blockIdx.x + (u0 == 0)) * kSlot;
+#pragma unroll
+                for (int d = 0; d < 2 * NG; ++d)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) __stcg(to + ((d * NT + t) * 4 + i) * 32 + lane, s.o[d][t][i]);
+                if (r == 0) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            __stcg(reinterpret_cast<float2*>(to + NT * 8 * NG * 32) + t * 8 + 2 * c + i, make_float2(s.off[t][i], s.l[t][i]));
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t others = (uint32_t)(c_last - c_first);
+                    const bool last = um::atom_acq_rel_add_u32(&p.tickets[c_first], 1u) == others;
+                    if (last) p.tickets[c_first] = 0;             // for the next call
+                    misc[4] = last;
+                }
+            }
+            __syncthreads();
+            if (misc[4]) {
+                s.clear();
+                for (int o = c_first + warp; o <= c_last; o += W) {
+                    const float* from = p.part + (size_t)(2 * o + (o == c_first)) * kSlot;
+                    float v[2 * NG][NT][4];
+                    float2 w[NT][2];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) w[t][i] = __ldcg(reinterpret_cast<const float2*>(from + NT * 8 * NG * 32) + t * 8 + 2 * c + i);
+#pragma unroll
+                    for (int d = 0; d < 2 * NG; ++d)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[d][t][i] = __ldcg(from + ((d * NT + t) * 4 + i) * 32 + lane);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float m = fmaxf(s.off[t][i], w[t][i].x), base = m == -INFINITY ? 0.f : m;
+                            const float f = ex2(s.off[t][i] - base), g = ex2(w[t][i].x - base);
+                            s.off[t][i] = m;
+                            s.l[t][i] = s.l[t][i] * f + w[t][i].y * g;
+#pragma unroll
+                            for (int d = 0; d < 2 * NG; ++d) {
+                                s.o[d][t][i] = s.o[d][t][i] * f + v[d][t][i] * g;
+                                s.o[d][t][i + 2] = s.o[d][t][i + 2] * f + v[d][t][i + 2] * g;
+                            }
+                        }
+                }
+                join_warps();
+                if (warp == 0) write_out();
+            }
+        }
+        x += u1 - u0;
+        if (x < hi) {
+            at.u = u1 - 1;
+            at.advance(p, 1);
+        }
+    }
+    // copies that were asked for and not used (a wait that ran out) land before the block ends
+    if (failed) {
+        for (int i = 0; i < NS; ++i)
+            if ((issued >> i) & 1u) {
+                const unsigned long long t0 = now_ns();
+                while (!ub_try(&my_bar[i], (phases >> i) & 1u) && now_ns() - t0 < 20000000ull) {}
+            }
+    }
+}
+
+constexpr int kWarps = 4;
+constexpr int kMaxOcc = 6;            // blocks of an SM, at most
+
+template <int NG, int NT> constexpr int stages() { return NG == 2 ? 4 : NG == 4 ? 3 : 2; }
+template <int NG, int NT> constexpr size_t smem_bytes() {
+    return (size_t)kWarps * stages<NG, NT>() * 1280 * NG + Smem<NG, NT, kWarps>::kJoin + kWarps * 8 * NT * 8 + kWarps * stages<NG, NT>() * 8 +
+           (kWarps + 1) * 8 + 64;
+}
+size_t slot_floats(int ng, int nt) { return (size_t)nt * 8 * ng * 32 + 16 * nt; }
+int most_rows(int ng) { return ng == 8 ? 2 : 4; }     // 8-row tiles that a warp's registers hold
+
+template <typename T, int NG, int NT>
+cudaError_t go(const spffn_kv4_ctx& c, const KParams& p, cudaStream_t st) {
+    auto kern = k_attend<T, NG, NT, kWarps, stages<NG, NT>()>;
+    constexpr size_t smem = smem_bytes<NG, NT>();
+    static int occ = 0;                                // of the kernel: the same on every sm_100a device
+    if (occ == 0) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        int n = 0;
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 32 * kWarps, smem);
+        if (e != cudaSuccess) return e;
+        occ = std::max(1, std::min(n, kMaxOcc));
+    }
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(c.sms * occ));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <typename T>
+cudaError_t by_shape(const spffn_kv4_ctx& c, const KParams& p, int nt, cudaStream_t st) {
+    switch (c.cfg.dh) {
+        case 64: return nt == 1 ? go<T, 2, 1>(c, p, st) : nt == 2 ? go<T, 2, 2>(c, p, st) : go<T, 2, 4>(c, p, st);
+        case 128: return nt == 1 ? go<T, 4, 1>(c, p, st) : nt == 2 ? go<T, 4, 2>(c, p, st) : go<T, 4, 4>(c, p, st);
+        default: return nt == 1 ? go<T, 8, 1>(c, p, st) : go<T, 8, 2>(c, p, st);
+    }
 }
 
 }  // namespace
 
 Layout layout(const spffn_kv4_config& c, int sms) {
     Layout l;
+    const int ng = c.dh / 32;
     l.ctl = 0;
     l.tickets = kCtlBytes;
-    l.part = kCtlBytes;
-    l.total = kCtlBytes;
+    l.part = align_up(l.tickets + (size_t)sms * kMaxOcc * sizeof(uint32_t), 256);
+    l.total = l.part + (size_t)2 * sms * kMaxOcc * slot_floats(ng, most_rows(ng)) * sizeof(float);
     return l;
 }
 
 cudaError_t launch_attend(const spffn_kv4_ctx& c, const AttendArgs& a, cudaStream_t st) {
-    const KParams p{a, c.pool, c.cfg.nh, c.cfg.kvh};
-    const int64_t warps = (int64_t)a.b.T * c.cfg.nh;
-    const unsigned grid = (unsigned)((warps + 3) / 4);
-    auto go = [&](auto tag) {
-        using T = decltype(tag);
-        if (c.cfg.dh == 64) k_attend_plain<T, 2><<<grid, 128, 0, st>>>(p);
-        else if (c.cfg.dh == 128) k_attend_plain<T, 4><<<grid, 128, 0, st>>>(p);
-        else k_attend_plain<T, 8><<<grid, 128, 0, st>>>(p);
-    };
-    if (c.cfg.dtype == SPFFN_BF16) go(__nv_bfloat16());
-    else go(__half());
-    return cudaGetLastError();
+    KParams p;
+    p.a = a;
+    p.pool = c.pool;
+    p.part = reinterpret_cast<float*>(c.ws + c.lay.part);
+    p.tickets = reinterpret_cast<uint32_t*>(c.ws + c.lay.tickets);
+    p.nh = c.cfg.nh;
+    p.kvh = c.cfg.kvh;
+    p.G = c.cfg.nh / c.cfg.kvh;
+    p.qvec = aligned_to(a.q, 16) && a.ldq % 8 == 0;
+    p.ovec = aligned_to(a.out, 8) && a.ldo % 4 == 0;
+    // 8, 16 or 32 query rows a tile, by the rows that a kv head has in the mean
+    const int64_t rows = ((int64_t)a.b.T + a.b.B - 1) / a.b.B * p.G;
+    const int nt = std::min(rows <= 8 ? 1 : rows <= 16 ? 2 : 4, most_rows(c.cfg.dh / 32));
+    return c.cfg.dtype == SPFFN_BF16 ? by_shape<__nv_bfloat16>(c, p, nt, st) : by_shape<__half>(c, p, nt, st);
 }
 
 }  // namespace kv4
