@@ -15,7 +15,8 @@
 // q is brought to [2^9, 2^10) by a power of two per row (exact), so a bf16 q fits fp16; the sums of
 // q_g enter as a high and a low half.  Probabilities are rounded to fp16 once alone and once times
 // the step (2^-11 each, against 2^-9 or 2^-12 of the output's own rounding); they are kept as
-// 2^(15 - R) p, R the largest exponent of a V step seen, so that p s stays in fp16's normal range.
+// 2^(7 - R) p and up to 2^8 more before the reference moves, R an exponent above every V step seen, so
+// that p s stays in fp16's range.
 //
 // Work: a unit is 32 positions of one (sequence, kv head, tile of query rows).  The units of the
 // batch are one line, cut into equal shares, one a block; blocks find their share from the lengths
@@ -48,12 +49,19 @@ struct KParams {
     uint32_t* tickets;                // [grid]
     int nh, kvh, G;
     int qvec, ovec;                   // rows of q in 16-byte pieces, rows of out in 8-byte pieces
+    uint32_t head_bytes, page_bytes;  // of one kv head of a page, and of a page
 };
 
 __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same with nothing to add to
+__device__ __forceinline__ void mma0(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     uint32_t d;
@@ -252,33 +260,41 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
         page0 = pos < ahead.keys ? __ldg(row + (pos >> bt.page_log)) : -1;
         page1 = pos + 16 < ahead.keys ? (bt.page_log == 4 ? __ldg(row + (pos >> 4) + 1) : page0) : -1;
     };
+    auto source = [&](int page, int pp) {
+        return p.pool + (uint64_t)(uint32_t)page * p.page_bytes +
+               ((uint32_t)ahead.hk * p.head_bytes + (uint32_t)((pp & (bt.page - 1)) >> 4) * L::kBytes);
+    };
     auto ask = [&](int st) {
         valid &= ~(3u << (2 * st));
         issued &= ~(1u << st);
         if (x_ahead >= hi || failed) return;
         const int pos = ahead.u * kUnit;
         const bool in0 = (unsigned)page0 < (unsigned)bt.pages, in1 = (unsigned)page1 < (unsigned)bt.pages;
-        if ((pos < ahead.keys && !in0) || (pos + 16 < ahead.keys && !in1)) {
-            if (lane == 0) latch(bt.err, ERR_PAGE_RANGE);
-        }
-        valid |= ((in0 ? 1u : 0u) | (in1 ? 2u : 0u)) << (2 * st);
-        if (in0 || in1) {
+        if (in0 && in1 && bt.page_log > 4) {
+            valid |= 3u << (2 * st);
             issued |= 1u << st;
             if (lane == 0) {
-                const uint32_t dst = s32(my_ring + st * kTile);
-                auto src = [&](int page, int pp) {
-                    return p.pool + (((int64_t)page * p.kvh + ahead.hk) * (bt.page >> 4) + ((pp & (bt.page - 1)) >> 4)) * L::kBytes;
-                };
-                ub_expect(&my_bar[st], (in0 ? L::kBytes : 0) + (in1 ? L::kBytes : 0));
-                if (in0 && in1 && bt.page_log > 4) bulk_copy(dst, src(page0, pos), kTile, &my_bar[st]);
-                else {
-                    if (in0) bulk_copy(dst, src(page0, pos), L::kBytes, &my_bar[st]);
-                    if (in1) bulk_copy(dst + L::kBytes, src(page1, pos + 16), L::kBytes, &my_bar[st]);
+                ub_expect(&my_bar[st], kTile);
+                bulk_copy(s32(my_ring + st * kTile), source(page0, pos), kTile, &my_bar[st]);
+            }
+        } else {
+            if (((pos < ahead.keys && !in0) || (pos + 16 < ahead.keys && !in1)) && lane == 0) latch(bt.err, ERR_PAGE_RANGE);
+            valid |= ((in0 ? 1u : 0u) | (in1 ? 2u : 0u)) << (2 * st);
+            if (in0 || in1) {
+                issued |= 1u << st;
+                if (lane == 0) {
+                    const uint32_t dst = s32(my_ring + st * kTile);
+                    ub_expect(&my_bar[st], (in0 ? L::kBytes : 0) + (in1 ? L::kBytes : 0));
+                    if (in0) bulk_copy(dst, source(page0, pos), L::kBytes, &my_bar[st]);
+                    if (in1) bulk_copy(dst + L::kBytes, source(page1, pos + 16), L::kBytes, &my_bar[st]);
                 }
             }
         }
         x_ahead += W;
-        if (x_ahead < hi) ahead.advance(p, W);
+        if (x_ahead < hi) {
+            ahead.u += W;
+            if (ahead.u >= ahead.units) ahead.advance(p, 0);
+        }
         look_up();
     };
     look_up();
@@ -299,7 +315,7 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
             for (int i = 0; i < 4; ++i) oz[t][i] = 0.f;
         // q of row r as the second operand, its group sums as halves, the factor of the columns' scores
         uint32_t qf[NT][NG][4], qs[NT][2];
-        float fq[NT][2], mx[NT][2];
+        float fq[NT][2];
         int pos[NT][2];
         int vexp = 0;                                             // R: V steps seen are below 2^R
         const int rows = at.n * p.G;
@@ -366,7 +382,6 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
             for (int i = 0; i < 2; ++i) {
                 const int rw = at.rt * R + t * 8 + 2 * c + i;
                 pos[t][i] = at.len - at.n + rw / p.G;             // of rows past the last: never written
-                mx[t][i] = -INFINITY;
             }
         }
         const int clear_to = at.len - at.n + at.rt * R / p.G + 1; // positions that every row sees
@@ -401,6 +416,8 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
                 uint32_t nan_tok = 0;                             // bit t: position p0 + t has such a step
                 __half2 top = __float2half2_rn(0.f);
                 auto tops = [&]() {
+                    // an upper bound by a factor of 4 at most: sums over groups run beside the integer pipe that
+                    // maxima and masks fill; a sum that overflows is held at R = 16 below
                     top = __float2half2_rn(0.f);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -410,7 +427,11 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
                             uint32_t v[NG];
                             lds<NG>(v, tile + j * L::kBytes + L::kVs + h * 16 * NG + c * 4 * NG);
 #pragma unroll
-                            for (int g = 0; g < NG; ++g) top = __hmax2_nan(top, as_h2(v[g]));
+                            for (int g = 0; g < NG; g += NG > 4 ? 4 : NG) {
+                                __half2 sum = __hadd2(as_h2(v[g]), as_h2(v[g + 1]));
+                                if constexpr (NG >= 4) sum = __hadd2(sum, __hadd2(as_h2(v[g + 2]), as_h2(v[g + 3])));
+                                top = __hmax2_nan(top, sum);
+                            }
                         }
                     }
 #pragma unroll
@@ -440,7 +461,7 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
                     tops();
                 }
                 const float vt = fmaxf(__low2float(top), __high2float(top));
-                const int ve = (int)(__float_as_uint(vt) >> 23) - 126;                          // vt < 2^ve
+                const int ve = min((int)(__float_as_uint(vt) >> 23) - 126, 16);                 // steps are below 2^ve
                 const int vnew = max(vexp, ve);
 
                 // scores of the unit: position r (and r + 8) of each block of 16, columns 2c, 2c + 1
@@ -460,11 +481,7 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
                     }
                     float part[NT][4];
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) part[t][i] = sc[j][t][i] = 0.f;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) mma(sc[j][t], z0, z1, z0, z1, qs[t][0], qs[t][1]);
+                    for (int t = 0; t < NT; ++t) mma0(sc[j][t], z0, z1, z0, z1, qs[t][0], qs[t][1]);
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
                         const float2 s0 = __half22float2(as_h2(st0[g >> 1])), s1 = __half22float2(as_h2(st1[g >> 1]));
@@ -475,13 +492,11 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
                                        b3 = (w1[g] >> 8) & 0x00f000f0u;
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            float d[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma(d, a0, a1, a2, a3, qf[t][g][0], qf[t][g][1]);
+                            float d[4];
+                            mma0(d, a0, a1, a2, a3, qf[t][g][0], qf[t][g][1]);
                             mma(d, b0, b1, b2, b3, qf[t][g][2], qf[t][g][3]);
-                            part[t][0] = fmaf(d[0], k0, part[t][0]);
-                            part[t][1] = fmaf(d[1], k0, part[t][1]);
-                            part[t][2] = fmaf(d[2], k1, part[t][2]);
-                            part[t][3] = fmaf(d[3], k1, part[t][3]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) part[t][i] = g == 0 ? d[i] * (i < 2 ? k0 : k1) : fmaf(d[i], i < 2 ? k0 : k1, part[t][i]);
                         }
                     }
 #pragma unroll
@@ -501,38 +516,39 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
                                 else if ((nan_tok >> tok) & 1u) sc[j][t][i] = __int_as_float(0x7fc00000);
                             }
                 }
-                // running maximum, and what it does to the state
-                bool moved = false;
-                float f[NT][2];
+                // The reference exponent moves only where a score passes it by more than fp16 has room for
+                // (2^8), or a larger V step needs that room; p is then at most 2^(15 - R).
+                float top_s[NT][2];
+                bool far = vnew > vexp;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float m = fmaxf(fmaxf(sc[0][t][i], sc[0][t][i + 2]), fmaxf(sc[1][t][i], sc[1][t][i + 2]));
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        m = fmaxf(m, mx[t][i]);
-                        mx[t][i] = m;
-                        const float off = m == -INFINITY ? -INFINITY : m + (float)(vnew - 15);
-                        f[t][i] = off == s.off[t][i] ? 1.f : ex2(s.off[t][i] - off);
-                        moved |= f[t][i] != 1.f;
-                        s.off[t][i] = off;
+                        top_s[t][i] = fmaxf(fmaxf(sc[0][t][i], sc[0][t][i + 2]), fmaxf(sc[1][t][i], sc[1][t][i + 2]));
+                        far |= top_s[t][i] > s.off[t][i] + (float)(15 - vexp);
                     }
-                vexp = vnew;
-                if (__any_sync(0xffffffffu, moved)) {
+                if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            s.l[t][i] *= f[t][i];
-                            oz[t][i] *= f[t][i];
-                            oz[t][i + 2] *= f[t][i];
+                            float m = top_s[t][i];
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                            m = fmaxf(m, s.off[t][i] - (float)(vexp - 7));
+                            const float off = m + (float)(vnew - 7);                    // -inf stays
+                            const float f = off == s.off[t][i] ? 1.f : ex2(s.off[t][i] - off);
+                            s.off[t][i] = off;
+                            s.l[t][i] *= f;
+                            oz[t][i] *= f;
+                            oz[t][i + 2] *= f;
 #pragma unroll
                             for (int d = 0; d < 2 * NG; ++d) {
-                                s.o[d][t][i] *= f[t][i];
-                                s.o[d][t][i + 2] *= f[t][i];
+                                s.o[d][t][i] *= f;
+                                s.o[d][t][i + 2] *= f;
                             }
                         }
+                    vexp = vnew;
                 }
                 // probabilities, turned into the second operand of the output's product
                 uint32_t pb[2][NT][2];
@@ -543,8 +559,7 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
                         float pr[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float off = s.off[t][i & 1];
-                            pr[i] = ex2(sc[j][t][i] - (off == -INFINITY ? 0.f : off));
+                            pr[i] = ex2(sc[j][t][i] - fmaxf(s.off[t][i & 1], -3e38f));
                             s.l[t][i & 1] += pr[i];
                         }
                         pb[j][t][0] = transpose8(pack2(pr[0], pr[1]));
@@ -835,6 +850,8 @@ cudaError_t launch_attend(const spffn_kv4_ctx& c, const AttendArgs& a, cudaStrea
     p.kvh = c.cfg.kvh;
     p.G = c.cfg.nh / c.cfg.kvh;
     p.qvec = aligned_to(a.q, 16) && a.ldq % 8 == 0;
+    p.head_bytes = (uint32_t)(c.cfg.page_size / 16) * (20u * c.cfg.dh);
+    p.page_bytes = p.head_bytes * (uint32_t)c.cfg.kvh;
     p.ovec = aligned_to(a.out, 8) && a.ldo % 4 == 0;
     // 8, 16 or 32 query rows a tile, by the rows that a kv head has in the mean
     const int64_t rows = ((int64_t)a.b.T + a.b.B - 1) / a.b.B * p.G;
