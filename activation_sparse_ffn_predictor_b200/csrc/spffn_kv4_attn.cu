@@ -53,19 +53,19 @@ struct KParams {
 };
 
 __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // the same with nothing to add to
 __device__ __forceinline__ void mma0(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -166,8 +166,8 @@ template <int NG, int NT, int W> struct Smem {
     static constexpr int kJoin = (W / 2 > 0 ? W / 2 : 1) * NT * 8 * NG * 32 * 4;   // states of half the warps
 };
 
-template <typename T, int NG, int NT, int W, int NS>
-__global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
+template <typename T, int NG, int NT, int W, int NS, int MB>
+__global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     using L = Blk<NG>;
     constexpr int R = 8 * NT, DH = 32 * NG;
     constexpr uint32_t kTile = 2 * L::kBytes;
@@ -248,53 +248,51 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
     uint8_t* my_ring = ring + warp * NS * kTile;
     uint64_t* my_bar = bars + warp * NS;
     Place<R> ahead = at;                                          // the next unit to ask for
-    long long x_ahead = lo + warp;
-    if (x_ahead < hi) ahead.advance(p, warp);
+    const int share = (int)min(hi - lo, 0x7fffffffll);            // units of the block
+    int left = share - warp;                                      // of them, from `ahead` on
+    if (left > 0) ahead.advance(p, warp);
     int page0 = -1, page1 = -1;
-    uint32_t valid = 0, phases = 0, issued = 0;                   // 2 bits, 1 bit, 1 bit a stage
+    uint32_t lacks = 0, phase = 0;                                // blocks that were not copied, 2 bits a stage
     bool failed = false;
     auto look_up = [&]() {                                        // the pages of `ahead`, used one round later
-        if (x_ahead >= hi) return;
+        if (left <= 0) return;
         const int pos = ahead.u * kUnit;
-        const int32_t* row = bt.table + ahead.b * bt.ldt;
-        page0 = pos < ahead.keys ? __ldg(row + (pos >> bt.page_log)) : -1;
-        page1 = pos + 16 < ahead.keys ? (bt.page_log == 4 ? __ldg(row + (pos >> 4) + 1) : page0) : -1;
+        const int32_t* row = bt.table + ahead.b * bt.ldt + (pos >> bt.page_log);
+        page0 = pos < ahead.keys ? __ldg(row) : -1;
+        if (bt.page_log == 4) page1 = pos + 16 < ahead.keys ? __ldg(row + 1) : -1;
     };
     auto source = [&](int page, int pp) {
         return p.pool + (uint64_t)(uint32_t)page * p.page_bytes +
                ((uint32_t)ahead.hk * p.head_bytes + (uint32_t)((pp & (bt.page - 1)) >> 4) * L::kBytes);
     };
     auto ask = [&](int st) {
-        valid &= ~(3u << (2 * st));
-        issued &= ~(1u << st);
-        if (x_ahead >= hi || failed) return;
+        if (left <= 0 || failed) return;
         const int pos = ahead.u * kUnit;
-        const bool in0 = (unsigned)page0 < (unsigned)bt.pages, in1 = (unsigned)page1 < (unsigned)bt.pages;
-        if (in0 && in1 && bt.page_log > 4) {
-            valid |= 3u << (2 * st);
-            issued |= 1u << st;
+        uint64_t* bar = &my_bar[st];
+        const uint32_t dst = s32(my_ring + st * kTile);
+        if (lacks) lacks &= ~(3u << (2 * st));
+        if (bt.page_log > 4 && (unsigned)page0 < (unsigned)bt.pages) {
+            // one stretch; where the row's positions end in its first block the second comes along unread
             if (lane == 0) {
-                ub_expect(&my_bar[st], kTile);
-                bulk_copy(s32(my_ring + st * kTile), source(page0, pos), kTile, &my_bar[st]);
+                ub_expect(bar, kTile);
+                bulk_copy(dst, source(page0, pos), kTile, bar);
             }
         } else {
-            if (((pos < ahead.keys && !in0) || (pos + 16 < ahead.keys && !in1)) && lane == 0) latch(bt.err, ERR_PAGE_RANGE);
-            valid |= ((in0 ? 1u : 0u) | (in1 ? 2u : 0u)) << (2 * st);
-            if (in0 || in1) {
-                issued |= 1u << st;
-                if (lane == 0) {
-                    const uint32_t dst = s32(my_ring + st * kTile);
-                    ub_expect(&my_bar[st], (in0 ? L::kBytes : 0) + (in1 ? L::kBytes : 0));
-                    if (in0) bulk_copy(dst, source(page0, pos), L::kBytes, &my_bar[st]);
-                    if (in1) bulk_copy(dst + L::kBytes, source(page1, pos + 16), L::kBytes, &my_bar[st]);
+            const bool in0 = (unsigned)page0 < (unsigned)bt.pages, in1 = bt.page_log == 4 && (unsigned)page1 < (unsigned)bt.pages;
+            if (((pos < ahead.keys && !in0) || (bt.page_log == 4 && pos + 16 < ahead.keys && !in1)) && lane == 0) latch(bt.err, ERR_PAGE_RANGE);
+            lacks |= ((in0 ? 0u : 1u) | (in1 ? 0u : 2u)) << (2 * st);
+            if (lane == 0) {
+                if (!in0 && !in1) um::ub_arrive(bar);
+                else {
+                    ub_expect(bar, (in0 ? L::kBytes : 0) + (in1 ? L::kBytes : 0));
+                    if (in0) bulk_copy(dst, source(page0, pos), L::kBytes, bar);
+                    if (in1) bulk_copy(dst + L::kBytes, source(page1, pos + 16), L::kBytes, bar);
                 }
             }
         }
-        x_ahead += W;
-        if (x_ahead < hi) {
-            ahead.u += W;
-            if (ahead.u >= ahead.units) ahead.advance(p, 0);
-        }
+        left -= W;
+        ahead.u += W;
+        if (ahead.u >= ahead.units && left > 0) ahead.advance(p, 0);
         look_up();
     };
     look_up();
@@ -302,10 +300,9 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
     for (int i = 0; i < NS; ++i) ask(i);
 
     // -------------------------------------------------------------------- the block's heads
-    int st = 0;
-    long long x = lo;
-    while (x < hi) {
-        const int u0 = at.u, u1 = (int)min((long long)at.units, u0 + (hi - x));
+    int st = 0, x = 0;
+    while (x < share) {
+        const int u0 = at.u, u1 = min(at.units, u0 + (share - x));
         State<NG, NT> s;
         s.clear();
         float oz[NT][4];
@@ -387,23 +384,19 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
         const int clear_to = at.len - at.n + at.rt * R / p.G + 1; // positions that every row sees
 
         // the warp's units of this head
-        const int first = (int)((warp - (x - lo)) % W + W) % W;
+        const int first = (warp - x) & (W - 1);
         for (int u = u0 + first; u < u1 && !failed; u += W) {
             const uint8_t* tile = my_ring + st * kTile;
-            const uint32_t have = (valid >> (2 * st)) & 3u;
-            if ((issued >> st) & 1u) {
-                const uint32_t ph = (phases >> st) & 1u;
-                if (!ub_try(&my_bar[st], ph)) {
-                    const unsigned long long t0 = now_ns();
-                    while (!ub_try(&my_bar[st], ph)) {
-                        if (now_ns() - t0 > um::kUWaitNs) {
-                            failed = true;
-                            break;
-                        }
+            const uint32_t have = 3u & ~(lacks >> (2 * st));
+            if (!ub_try(&my_bar[st], phase)) {
+                const unsigned long long t0 = now_ns();
+                while (!ub_try(&my_bar[st], phase)) {
+                    if (now_ns() - t0 > um::kUWaitNs) {
+                        failed = true;
+                        break;
                     }
                 }
                 failed = __any_sync(0xffffffffu, failed);
-                phases ^= 1u << st;
             }
             if (failed) {
                 if (lane == 0) latch(bt.err, ERR_PIPE_TIMEOUT);
@@ -604,7 +597,10 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
             }
             __syncwarp();                                         // every lane has read the stage
             ask(st);
-            st = st + 1 == NS ? 0 : st + 1;
+            if (++st == NS) {
+                st = 0;
+                phase ^= 1;
+            }
         }
 
         // ------------------------------------------------ the warps' states become one
@@ -699,7 +695,7 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
                 }
         };
         join_warps();
-        const long long head_lo = x - u0;                         // the head's stretch of the line
+        const long long head_lo = lo + x - u0;                        // the head's stretch of the line
         const bool whole = u0 == 0 && u1 == at.units;
         if (whole) {
             if (warp == 0) write_out();
@@ -766,25 +762,30 @@ __global__ void __launch_bounds__(32 * W) k_attend(const KParams p) {
             }
         }
         x += u1 - u0;
-        if (x < hi) {
+        if (x < share) {
             at.u = u1 - 1;
             at.advance(p, 1);
         }
     }
-    // copies that were asked for and not used (a wait that ran out) land before the block ends
+    // copies that were asked for and not used (a wait that ran out) land before the block ends: the stages from
+    // st on are in the current phase, those before it one further
     if (failed) {
-        for (int i = 0; i < NS; ++i)
-            if ((issued >> i) & 1u) {
-                const unsigned long long t0 = now_ns();
-                while (!ub_try(&my_bar[i], (phases >> i) & 1u) && now_ns() - t0 < 20000000ull) {}
-            }
+        for (int i = 0; i < NS; ++i) {
+            const unsigned long long t0 = now_ns();
+            while (!ub_try(&my_bar[i], i >= st ? phase : phase ^ 1u) && now_ns() - t0 < 20000000ull) {}
+        }
     }
 }
 
+#ifndef KNS
+#define KNS 3
+#define KMB 3
+#endif
 constexpr int kWarps = 4;
 constexpr int kMaxOcc = 6;            // blocks of an SM, at most
 
-template <int NG, int NT> constexpr int stages() { return NG == 2 ? 4 : NG == 4 ? 3 : 2; }
+template <int NG, int NT> constexpr int stages() { return NG == 2 ? 4 : NG == 4 ? KNS : 2; }
+template <int NG, int NT> constexpr int blocks_at_once() { return NG == 4 && NT == 1 ? KMB : 1; }
 template <int NG, int NT> constexpr size_t smem_bytes() {
     return (size_t)kWarps * stages<NG, NT>() * 1280 * NG + Smem<NG, NT, kWarps>::kJoin + kWarps * 8 * NT * 8 + kWarps * stages<NG, NT>() * 8 +
            (kWarps + 1) * 8 + 64;
@@ -794,7 +795,7 @@ int most_rows(int ng) { return ng == 8 ? 2 : 4; }     // 8-row tiles that a warp
 
 template <typename T, int NG, int NT>
 cudaError_t go(const spffn_kv4_ctx& c, const KParams& p, cudaStream_t st) {
-    auto kern = k_attend<T, NG, NT, kWarps, stages<NG, NT>()>;
+    auto kern = k_attend<T, NG, NT, kWarps, stages<NG, NT>(), blocks_at_once<NG, NT>()>;
     constexpr size_t smem = smem_bytes<NG, NT>();
     static int occ = 0;                                // of the kernel: the same on every sm_100a device
     if (occ == 0) {
