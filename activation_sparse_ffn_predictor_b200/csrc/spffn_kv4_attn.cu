@@ -19,13 +19,13 @@
 // that p s stays in fp16's range.
 //
 // Work: a unit is 32 positions of one (sequence, kv head, tile of query rows).  The units of the
-// batch are one line, cut into equal shares, one a block; blocks find their share from the lengths
-// on the device (a captured graph replays with other lengths).  In a block the units go round the
-// warps; each warp streams its own through a ring of bulk copies (a unit is one stretch of a page,
+// batch are one line, cut into equal shares, one a warp or one a block; they are found from the lengths
+// on the device (a captured graph replays with other lengths).  In a block's share the units go round
+// the warps; each warp streams its own through a ring of bulk copies (a unit is one stretch of a page,
 // two where pages have 16 tokens) and nothing waits for another warp until a head's end, where
-// the warps' states are joined through shared memory.  A head that several blocks share leaves
-// its states in the workspace; the last block to arrive joins them in their order, so the result
-// does not depend on which it is.
+// the warps' states are joined through shared memory.  A head that several shares cut leaves its
+// states in the workspace; the last to arrive joins them in their order, so the result does not
+// depend on which it is.
 #include "spffn_umma.cuh"
 #include "spffn_kv4.cuh"
 
@@ -39,14 +39,17 @@ using um::ub_expect;
 using um::ub_init;
 using um::ub_try;
 
+#ifndef SOLO_MIN
+#define SOLO_MIN 200
+#endif
 constexpr int kUnit = 32;             // positions of a unit
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct KParams {
     AttendArgs a;
     const uint8_t* pool;
-    float* part;                      // [2 grid][slot floats]
-    uint32_t* tickets;                // [grid]
+    float* part;                      // [2 shares][slot floats]
+    uint32_t* tickets;                // [shares]
     int nh, kvh, G;
     int qvec, ovec;                   // rows of q in 16-byte pieces, rows of out in 8-byte pieces
     uint32_t head_bytes, page_bytes;  // of one kv head of a page, and of a page
@@ -162,22 +165,25 @@ template <int NG, int NT> struct State {
     }
 };
 
-template <int NG, int NT, int W> struct Smem {
-    static constexpr int kJoin = (W / 2 > 0 ? W / 2 : 1) * NT * 8 * NG * 32 * 4;   // states of half the warps
-};
+template <int NG, int W, bool SOLO> constexpr int join_bytes() { return SOLO ? 0 : W / 2 * 8 * NG * 32 * 4; }  // 8 rows of half the warps' states
 
-template <typename T, int NG, int NT, int W, int NS, int MB>
+// SOLO: every warp has a share of its own (many heads: nothing is joined through shared memory and no warp
+// waits for another); otherwise a block's warps go through one share together (few heads, long contexts).
+template <typename T, int NG, int NT, int W, int NS, int MB, bool SOLO>
 __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     using L = Blk<NG>;
+    constexpr int M = SOLO ? 1 : W;                               // warps of a share
+    constexpr int kSnap = SOLO ? 2 : W;
     constexpr int R = 8 * NT, DH = 32 * NG;
     constexpr uint32_t kTile = 2 * L::kBytes;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring = smem;                                         // [W][NS][kTile]
     float* join = reinterpret_cast<float*>(smem + W * NS * kTile);
-    float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(join) + Smem<NG, NT, W>::kJoin);   // [W][R]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(ml + W * R);     // [W][NS]
+    float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(join) + join_bytes<NG, W, SOLO>());   // [W][R], not SOLO
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ml + (SOLO ? 0 : W * R));     // [W][NS]
     long long* scan = reinterpret_cast<long long*>(bars + W * NS);
-    int* misc = reinterpret_cast<int*>(scan + W + 1);
+    long long* bound = scan + W;                                  // [W + 1] where the block's shares begin
+    int* misc = reinterpret_cast<int*>(bound + W + 1);            // [W][4], and one more
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const Batch& bt = p.a.b;
 
@@ -210,47 +216,57 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
         if (w < warp) pref += scan[w];
         total += scan[w];
     }
-    // no more blocks than there are rounds of the warps
-    const long long blocks = min((long long)gridDim.x, max(1ll, total / W));
-    if ((long long)blockIdx.x >= blocks) return;
-    const long long lo = total * blockIdx.x / blocks, hi = total * (blockIdx.x + 1) / blocks;
-    if (lo >= hi) return;
-    if (lo >= pref && lo < pref + mine) {
-        for (int s = threadIdx.x * per;; ++s) {
-            const long long here = units_of_seq(s);
-            if (lo < pref + here) {
-                const Seq q = seq_of(bt, s);
-                const long long of_head = here / p.kvh;
-                long long in = lo - pref;
-                int t = 0;
-                misc[0] = s;
-                misc[1] = (int)(in / of_head);
-                in %= of_head;
-                for (;; ++t) {
-                    const int u = Place<R>::units_of(Place<R>::keys_of(t, q.n, q.len, q.ok, p.G));
-                    if (in < u) break;
-                    in -= u;
-                }
-                misc[2] = t;
-                misc[3] = (int)in;
-                break;
+    // No more shares than there are units for their warps.  A share that would begin within kSnap units of
+    // a head's end begins at the end: cutting a head costs about as much as that many units.
+    const int shares = (int)min((long long)gridDim.x * (SOLO ? W : 1), max(1ll, total / M));
+    const int id0 = SOLO ? blockIdx.x * W : blockIdx.x, ids = SOLO ? W : 1;
+    if (total == 0 || id0 >= shares) return;
+    for (int k = 0; k <= ids; ++k) {
+        const long long raw = total * min(id0 + k, shares) / shares;
+        if (raw >= total) {
+            if (threadIdx.x == 0) bound[k] = total;
+        } else if (raw >= pref && raw < pref + mine) {
+            long long in = raw - pref;
+            int sq = threadIdx.x * per;
+            for (long long here; in >= (here = units_of_seq(sq)); ++sq) in -= here;
+            const Seq q = seq_of(bt, sq);
+            const long long of_head = units_of_seq(sq) / p.kvh;
+            int hk = (int)(in / of_head), t = 0, u;
+            in %= of_head;
+            while (in >= (u = Place<R>::units_of(Place<R>::keys_of(t, q.n, q.len, q.ok, p.G)))) {
+                in -= u;
+                ++t;
             }
-            pref += here;
+            const bool up = in > kSnap && u - in <= kSnap, down = in <= kSnap;
+            bound[k] = down ? raw - in : up ? raw + (u - in) : raw;
+            if (k < ids) {
+                int* m = misc + 4 * k;
+                m[0] = sq;
+                m[1] = hk;
+                m[2] = t;
+                m[3] = down ? 0 : (int)in;                        // one head further where it went up: see below
+                if (up) m[3] = u;
+            }
         }
     }
     __syncthreads();
-    Place<R> at;                                                  // where the block stands
-    at.b = misc[0]; at.hk = misc[1]; at.rt = misc[2]; at.u = misc[3];
+    const int id = id0 + (SOLO ? warp : 0);
+    const int wk = SOLO ? warp : 0;
+    if (id >= shares || bound[wk] >= bound[wk + 1]) return;       // in a block that shares, all warps alike
+    const long long lo = bound[wk], hi = bound[wk + 1];
+    Place<R> at;                                                  // where the share stands
+    at.b = misc[4 * wk]; at.hk = misc[4 * wk + 1]; at.rt = misc[4 * wk + 2]; at.u = misc[4 * wk + 3];
     at.load_seq(p);
     at.load_tile(p);
+    at.advance(p, 0);
 
     // ------------------------------------------------------------ the warp's ring of copies
     uint8_t* my_ring = ring + warp * NS * kTile;
     uint64_t* my_bar = bars + warp * NS;
     Place<R> ahead = at;                                          // the next unit to ask for
-    const int share = (int)min(hi - lo, 0x7fffffffll);            // units of the block
-    int left = share - warp;                                      // of them, from `ahead` on
-    if (left > 0) ahead.advance(p, warp);
+    const int share = (int)min(hi - lo, 0x7fffffffll);            // its units
+    int left = share - (SOLO ? 0 : warp);                         // of them, from `ahead` on
+    if (!SOLO && left > 0) ahead.advance(p, warp);
     int page0 = -1, page1 = -1;
     uint32_t lacks = 0, phase = 0;                                // blocks that were not copied, 2 bits a stage
     bool failed = false;
@@ -290,8 +306,8 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                 }
             }
         }
-        left -= W;
-        ahead.u += W;
+        left -= M;
+        ahead.u += M;
         if (ahead.u >= ahead.units && left > 0) ahead.advance(p, 0);
         look_up();
     };
@@ -299,7 +315,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
 #pragma unroll
     for (int i = 0; i < NS; ++i) ask(i);
 
-    // -------------------------------------------------------------------- the block's heads
+    // -------------------------------------------------------------------- the share's heads
     int st = 0, x = 0;
     while (x < share) {
         const int u0 = at.u, u1 = min(at.units, u0 + (share - x));
@@ -384,8 +400,8 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
         const int clear_to = at.len - at.n + at.rt * R / p.G + 1; // positions that every row sees
 
         // the warp's units of this head
-        const int first = (warp - x) & (W - 1);
-        for (int u = u0 + first; u < u1 && !failed; u += W) {
+        const int first = SOLO ? 0 : (warp - x) & (W - 1);
+        for (int u = u0 + first; u < u1 && !failed; u += M) {
             const uint8_t* tile = my_ring + st * kTile;
             const uint32_t have = 3u & ~(lacks >> (2 * st));
             if (!ub_try(&my_bar[st], phase)) {
@@ -622,6 +638,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                 }
             }
         auto join_warps = [&]() {                                 // warp 0 ends up with the sum
+            if constexpr (!SOLO) {
             if (r == 0) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
@@ -649,37 +666,42 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                         s.o[d][t][i + 2] *= f;
                     }
                 }
+            // half of the warps hand over at a time, 8 rows at a time
 #pragma unroll
-            for (int h = W / 2; h >= 1; h >>= 1) {
-                if (warp >= h && warp < 2 * h) {
-                    float* to = join + (size_t)(warp - h) * (NT * 8 * NG * 32) + lane;
+            for (int h = W / 2; h >= 1; h >>= 1)
 #pragma unroll
-                    for (int d = 0; d < 2 * NG; ++d)
+                for (int t = 0; t < NT; ++t) {
+                    float* at_join = join + (size_t)(warp & (h - 1)) * (8 * NG * 32) + lane;
+                    if (warp >= h && warp < 2 * h) {
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
+                        for (int d = 0; d < 2 * NG; ++d)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) to[((d * NT + t) * 4 + i) * 32] = s.o[d][t][i];
+                            for (int i = 0; i < 4; ++i) at_join[(4 * d + i) * 32] = s.o[d][t][i];
+                    }
+                    __syncthreads();
+                    if (warp < h) {
+#pragma unroll
+                        for (int d = 0; d < 2 * NG; ++d)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) s.o[d][t][i] += at_join[(4 * d + i) * 32];
+                    }
+                    if (h > 1 || t + 1 < NT) __syncthreads();
                 }
-                __syncthreads();
-                if (warp < h) {
-                    const float* from = join + (size_t)warp * (NT * 8 * NG * 32) + lane;
-#pragma unroll
-                    for (int d = 0; d < 2 * NG; ++d)
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) s.o[d][t][i] += from[((d * NT + t) * 4 + i) * 32];
-                }
-                if (h > 1) __syncthreads();
             }
         };
+        const bool speaks = SOLO || warp == 0;                    // has the share's state
+        bool row_in[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) row_in[t][i] = at.rt * R + t * 8 + 2 * c + i < rows;
         auto write_out = [&]() {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int row = at.rt * R + t * 8 + 2 * c + i;
-                    if (row >= rows) continue;
+                    if (!row_in[t][i]) continue;
                     T* to = static_cast<T*>(p.a.out) + (int64_t)(at.row0 + row / p.G) * p.a.ldo + (int64_t)(at.hk * p.G + row % p.G) * DH + 4 * r;
                     const float inv = s.l[t][i] == 0.f ? 0.f : 1.f / s.l[t][i];
 #pragma unroll
@@ -695,53 +717,60 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                 }
         };
         join_warps();
-        const long long head_lo = lo + x - u0;                        // the head's stretch of the line
-        const bool whole = u0 == 0 && u1 == at.units;
-        if (whole) {
-            if (warp == 0) write_out();
+        if (u0 == 0 && u1 == at.units) {
+            if (speaks) write_out();
         } else {
+            // the head's stretch of the line and the shares whose cuts fall inside it, as the plan above cuts
             constexpr int kSlot = NT * 8 * NG * 32 + 2 * R;
-            const int c_first = (int)(((head_lo + 1) * blocks - 1) / total), c_last = (int)(((head_lo + at.units) * blocks - 1) / total);
-            if (warp == 0) {
-                float* to = p.part + (size_t)(2 * blockIdx.x + (u0 == 0)) * kSlot;
+            const long long head_lo = lo + x - u0;
+            const int c_first = (int)(((head_lo + kSnap + 1) * shares + total - 1) / total) - 1;
+            const int c_last = (int)(((head_lo + at.units - kSnap) * shares + total - 1) / total) - 1;
+            bool last = false;
+            if (speaks) {
+                float* to = p.part + (size_t)(2 * id + (u0 == 0)) * kSlot;
 #pragma unroll
-                for (int d = 0; d < 2 * NG; ++d)
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                    for (int i = 0; i < 2; ++i) {
+                        if (!row_in[t][i]) continue;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) __stcg(to + ((d * NT + t) * 4 + i) * 32 + lane, s.o[d][t][i]);
-                if (r == 0) {
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
+                        for (int d = 0; d < 2 * NG; ++d) {
+                            __stcg(to + ((d * NT + t) * 4 + i) * 32 + lane, s.o[d][t][i]);
+                            __stcg(to + ((d * NT + t) * 4 + i + 2) * 32 + lane, s.o[d][t][i + 2]);
+                        }
+                        if (r == 0)
                             __stcg(reinterpret_cast<float2*>(to + NT * 8 * NG * 32) + t * 8 + 2 * c + i, make_float2(s.off[t][i], s.l[t][i]));
-                }
+                    }
                 __syncwarp();
                 if (lane == 0) {
-                    const uint32_t others = (uint32_t)(c_last - c_first);
-                    const bool last = um::atom_acq_rel_add_u32(&p.tickets[c_first], 1u) == others;
+                    last = um::atom_acq_rel_add_u32(&p.tickets[c_first], 1u) == (uint32_t)(c_last - c_first);
                     if (last) p.tickets[c_first] = 0;             // for the next call
-                    misc[4] = last;
                 }
+                last = __shfl_sync(0xffffffffu, last, 0);
+                if (!SOLO && lane == 0) misc[4 * W] = last;
             }
-            __syncthreads();
-            if (misc[4]) {
+            if constexpr (!SOLO) {
+                __syncthreads();
+                last = misc[4 * W];
+            }
+            if (last) {
                 s.clear();
-                for (int o = c_first + warp; o <= c_last; o += W) {
+                for (int o = c_first + (SOLO ? 0 : warp); o <= c_last; o += M) {
                     const float* from = p.part + (size_t)(2 * o + (o == c_first)) * kSlot;
                     float v[2 * NG][NT][4];
                     float2 w[NT][2];
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) w[t][i] = __ldcg(reinterpret_cast<const float2*>(from + NT * 8 * NG * 32) + t * 8 + 2 * c + i);
+                        for (int i = 0; i < 2; ++i) {
+                            const bool in = row_in[t][i];
+                            w[t][i] = in ? __ldcg(reinterpret_cast<const float2*>(from + NT * 8 * NG * 32) + t * 8 + 2 * c + i) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-                    for (int d = 0; d < 2 * NG; ++d)
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[d][t][i] = __ldcg(from + ((d * NT + t) * 4 + i) * 32 + lane);
+                            for (int d = 0; d < 2 * NG; ++d) {
+                                v[d][t][i] = in ? __ldcg(from + ((d * NT + t) * 4 + i) * 32 + lane) : 0.f;
+                                v[d][t][i + 2] = in ? __ldcg(from + ((d * NT + t) * 4 + i + 2) * 32 + lane) : 0.f;
+                            }
+                        }
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -758,7 +787,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                         }
                 }
                 join_warps();
-                if (warp == 0) write_out();
+                if (speaks) write_out();
             }
         }
         x += u1 - u0;
@@ -777,40 +806,34 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     }
 }
 
-#ifndef KNS
-#define KNS 3
-#define KMB 3
-#endif
-constexpr int kWarps = 4;
-constexpr int kMaxOcc = 6;            // blocks of an SM, at most
-
-template <int NG, int NT> constexpr int stages() { return NG == 2 ? 4 : NG == 4 ? KNS : 2; }
-template <int NG, int NT> constexpr int blocks_at_once() { return NG == 4 && NT == 1 ? KMB : 1; }
-template <int NG, int NT> constexpr size_t smem_bytes() {
-    return (size_t)kWarps * stages<NG, NT>() * 1280 * NG + Smem<NG, NT, kWarps>::kJoin + kWarps * 8 * NT * 8 + kWarps * stages<NG, NT>() * 8 +
-           (kWarps + 1) * 8 + 64;
+// The shapes of a launch: warps and blocks at once as registers and the rings allow.
+template <int NG, int NT, bool SOLO> struct Shape {
+    static constexpr int W = SOLO ? 4 : NT == 1 ? (NG == 8 ? 8 : 16) : NT == 2 && NG < 8 ? 8 : 8;
+    static constexpr int NS = NG == 2 ? 4 : 2;
+    static constexpr int MB = SOLO ? (NG == 2 ? 4 : NG == 4 ? 3 : 2) : 1;
+    static constexpr size_t smem = (size_t)W * NS * 1280 * NG + join_bytes<NG, W, SOLO>() + (SOLO ? 0 : W * 8 * NT * 8) + W * NS * 8 +
+                                   (2 * W + 1) * 8 + (4 * W + 1) * 4 + 16;
+    static_assert(smem <= 227 * 1024 / MB - 1024, "");
+    static constexpr int shares = MB * (SOLO ? W : 1);           // of an SM
+    static constexpr size_t part_floats = (size_t)2 * shares * (NT * 8 * NG * 32 + 16 * NT);
+};
+constexpr int kMaxShares = 16;                                    // of an SM
+int most_rows(int ng) { return ng == 8 ? 2 : 4; }                 // 8-row tiles that a warp's registers hold
+template <int NG> constexpr size_t part_floats() {
+    return std::max(std::max(Shape<NG, 1, true>::part_floats, Shape<NG, 1, false>::part_floats),
+                    std::max(Shape<NG, 2, false>::part_floats, NG == 8 ? (size_t)0 : Shape<NG, 4, false>::part_floats));
 }
-size_t slot_floats(int ng, int nt) { return (size_t)nt * 8 * ng * 32 + 16 * nt; }
-int most_rows(int ng) { return ng == 8 ? 2 : 4; }     // 8-row tiles that a warp's registers hold
 
-template <typename T, int NG, int NT>
+template <typename T, int NG, int NT, bool SOLO>
 cudaError_t go(const spffn_kv4_ctx& c, const KParams& p, cudaStream_t st) {
-    auto kern = k_attend<T, NG, NT, kWarps, stages<NG, NT>(), blocks_at_once<NG, NT>()>;
-    constexpr size_t smem = smem_bytes<NG, NT>();
-    static int occ = 0;                                // of the kernel: the same on every sm_100a device
-    if (occ == 0) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        int n = 0;
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 32 * kWarps, smem);
-        if (e != cudaSuccess) return e;
-        occ = std::max(1, std::min(n, kMaxOcc));
-    }
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    using S = Shape<NG, NT, SOLO>;
+    auto kern = k_attend<T, NG, NT, S::W, S::NS, S::MB, SOLO>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(c.sms * occ));
-    cfg.blockDim = dim3(32 * kWarps);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3((unsigned)(c.sms * S::MB));
+    cfg.blockDim = dim3(32 * S::W);
+    cfg.dynamicSmemBytes = S::smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -820,12 +843,21 @@ cudaError_t go(const spffn_kv4_ctx& c, const KParams& p, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+template <typename T, int NG>
+cudaError_t by_rows(const spffn_kv4_ctx& c, const KParams& p, int nt, bool solo, cudaStream_t st) {
+    if (nt == 1) return solo ? go<T, NG, 1, true>(c, p, st) : go<T, NG, 1, false>(c, p, st);
+    if constexpr (NG < 8) {
+        if (nt == 4) return go<T, NG, 4, false>(c, p, st);
+    }
+    return go<T, NG, 2, false>(c, p, st);
+}
+
 template <typename T>
-cudaError_t by_shape(const spffn_kv4_ctx& c, const KParams& p, int nt, cudaStream_t st) {
+cudaError_t by_width(const spffn_kv4_ctx& c, const KParams& p, int nt, bool solo, cudaStream_t st) {
     switch (c.cfg.dh) {
-        case 64: return nt == 1 ? go<T, 2, 1>(c, p, st) : nt == 2 ? go<T, 2, 2>(c, p, st) : go<T, 2, 4>(c, p, st);
-        case 128: return nt == 1 ? go<T, 4, 1>(c, p, st) : nt == 2 ? go<T, 4, 2>(c, p, st) : go<T, 4, 4>(c, p, st);
-        default: return nt == 1 ? go<T, 8, 1>(c, p, st) : go<T, 8, 2>(c, p, st);
+        case 64: return by_rows<T, 2>(c, p, nt, solo, st);
+        case 128: return by_rows<T, 4>(c, p, nt, solo, st);
+        default: return by_rows<T, 8>(c, p, nt, solo, st);
     }
 }
 
@@ -833,11 +865,11 @@ cudaError_t by_shape(const spffn_kv4_ctx& c, const KParams& p, int nt, cudaStrea
 
 Layout layout(const spffn_kv4_config& c, int sms) {
     Layout l;
-    const int ng = c.dh / 32;
+    const size_t part = c.dh == 64 ? part_floats<2>() : c.dh == 128 ? part_floats<4>() : part_floats<8>();
     l.ctl = 0;
     l.tickets = kCtlBytes;
-    l.part = align_up(l.tickets + (size_t)sms * kMaxOcc * sizeof(uint32_t), 256);
-    l.total = l.part + (size_t)2 * sms * kMaxOcc * slot_floats(ng, most_rows(ng)) * sizeof(float);
+    l.part = align_up(l.tickets + (size_t)sms * kMaxShares * sizeof(uint32_t), 256);
+    l.total = l.part + sms * part * sizeof(float);
     return l;
 }
 
@@ -857,7 +889,8 @@ cudaError_t launch_attend(const spffn_kv4_ctx& c, const AttendArgs& a, cudaStrea
     // 8, 16 or 32 query rows a tile, by the rows that a kv head has in the mean
     const int64_t rows = ((int64_t)a.b.T + a.b.B - 1) / a.b.B * p.G;
     const int nt = std::min(rows <= 8 ? 1 : rows <= 16 ? 2 : 4, most_rows(c.cfg.dh / 32));
-    return c.cfg.dtype == SPFFN_BF16 ? by_shape<__nv_bfloat16>(c, p, nt, st) : by_shape<__half>(c, p, nt, st);
+    const bool solo = (int64_t)a.b.B * c.cfg.kvh >= SOLO_MIN;
+    return c.cfg.dtype == SPFFN_BF16 ? by_width<__nv_bfloat16>(c, p, nt, solo, st) : by_width<__half>(c, p, nt, solo, st);
 }
 
 }  // namespace kv4
