@@ -103,6 +103,11 @@ template <int N> __device__ __forceinline__ void lds(uint32_t* w, const uint8_t*
     }
 }
 
+// 64-bit by 64-bit, in 32 bits where both fit (the usual case by far: a 64-bit division is some hundred cycles)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // A place in the line of units: (sequence, kv head, row tile, unit of it).  Pairs that differ in
 // the row tile alone are neighbours, so their positions come from L2 the second time.
 template <int R> struct Place {
@@ -115,7 +120,8 @@ template <int R> struct Place {
         nrt = (n * p.G + R - 1) / R;
     }
     static __device__ __forceinline__ int keys_of(int rt, int n, int len, bool ok, int G) {
-        return ok ? len - n + (min((rt + 1) * R, n * G) - 1) / G + 1 : 0;
+        if (!ok) return 0;
+        return (rt + 1) * R >= n * G ? len : len - n + ((rt + 1) * R - 1) / G + 1;
     }
     // a sequence whose length was refused keeps one unit a tile, without positions: its rows become 0
     static __device__ __forceinline__ int units_of(int keys) { return max(1, (keys + kUnit - 1) / kUnit); }
@@ -173,7 +179,7 @@ template <typename T, int NG, int NT, int W, int NS, int MB, bool SOLO>
 __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     using L = Blk<NG>;
     constexpr int M = SOLO ? 1 : W;                               // warps of a share
-    constexpr int kSnap = SOLO ? 2 : W;
+    constexpr int kSnap = SOLO ? 2 : W, kLeast = SOLO ? 1 : 2;
     constexpr int R = 8 * NT, DH = 32 * NG;
     constexpr uint32_t kTile = 2 * L::kBytes;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -181,9 +187,9 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     float* join = reinterpret_cast<float*>(smem + W * NS * kTile);
     float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(join) + join_bytes<NG, W, SOLO>());   // [W][R], not SOLO
     uint64_t* bars = reinterpret_cast<uint64_t*>(ml + (SOLO ? 0 : W * R));     // [W][NS]
-    long long* scan = reinterpret_cast<long long*>(bars + W * NS);
-    long long* bound = scan + W;                                  // [W + 1] where the block's shares begin
-    int* misc = reinterpret_cast<int*>(bound + W + 1);            // [W][4], and one more
+    int64_t* scan = reinterpret_cast<int64_t*>(bars + W * NS);    // [W]
+    int64_t* starts = scan + W;                                   // [threads]
+    int* s_last = reinterpret_cast<int*>(starts + 32 * W);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const Batch& bt = p.a.b;
 
@@ -192,70 +198,82 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     um::pdl_trigger();
     um::pdl_wait();
-    const int per = (bt.B + 32 * W - 1) / (32 * W);
-    auto units_of_seq = [&](int s) -> long long {
-        const Seq q = seq_of(bt, s);
+    constexpr int kThreads = 32 * W;
+    const int per = (bt.B + kThreads - 1) / kThreads;
+    auto units_of_head = [&](const Seq& q) -> int64_t {           // of each kv head of a sequence
         const int nrt = (q.n * p.G + R - 1) / R;
-        long long sum = 0;
+        int64_t sum = 0;
         for (int t = 0; t < nrt; ++t) sum += Place<R>::units_of(Place<R>::keys_of(t, q.n, q.len, q.ok, p.G));
-        return sum * p.kvh;
+        return sum;
     };
-    long long mine = 0;
-    for (int s = threadIdx.x * per; s < min(bt.B, ((int)threadIdx.x + 1) * per); ++s) mine += units_of_seq(s);
-    long long pref = mine;
+    int64_t mine = 0;
+    for (int i = 0, sq = threadIdx.x * per; i < per && sq < bt.B; ++i, ++sq) mine += units_of_head(seq_of(bt, sq)) * p.kvh;
+    int64_t pref = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, pref, o);
+        const int64_t v = __shfl_up_sync(0xffffffffu, pref, o);
         if (lane >= o) pref += v;
     }
     if (lane == 31) scan[warp] = pref;
     __syncthreads();
-    long long total = 0;
-    pref -= mine;
+    int64_t total = 0, below = 0;
+#pragma unroll
     for (int w = 0; w < W; ++w) {
-        if (w < warp) pref += scan[w];
+        if (w < warp) below += scan[w];
         total += scan[w];
     }
-    // No more shares than there are units for their warps.  A share that would begin within kSnap units of
-    // a head's end begins at the end: cutting a head costs about as much as that many units.
-    const int shares = (int)min((long long)gridDim.x * (SOLO ? W : 1), max(1ll, total / M));
-    const int id0 = SOLO ? blockIdx.x * W : blockIdx.x, ids = SOLO ? W : 1;
-    if (total == 0 || id0 >= shares) return;
-    for (int k = 0; k <= ids; ++k) {
-        const long long raw = total * min(id0 + k, shares) / shares;
-        if (raw >= total) {
-            if (threadIdx.x == 0) bound[k] = total;
-        } else if (raw >= pref && raw < pref + mine) {
-            long long in = raw - pref;
-            int sq = threadIdx.x * per;
-            for (long long here; in >= (here = units_of_seq(sq)); ++sq) in -= here;
-            const Seq q = seq_of(bt, sq);
-            const long long of_head = units_of_seq(sq) / p.kvh;
-            int hk = (int)(in / of_head), t = 0, u;
-            in %= of_head;
-            while (in >= (u = Place<R>::units_of(Place<R>::keys_of(t, q.n, q.len, q.ok, p.G)))) {
-                in -= u;
-                ++t;
-            }
-            const bool up = in > kSnap && u - in <= kSnap, down = in <= kSnap;
-            bound[k] = down ? raw - in : up ? raw + (u - in) : raw;
-            if (k < ids) {
-                int* m = misc + 4 * k;
-                m[0] = sq;
-                m[1] = hk;
-                m[2] = t;
-                m[3] = down ? 0 : (int)in;                        // one head further where it went up: see below
-                if (up) m[3] = u;
-            }
-        }
-    }
+    starts[threadIdx.x] = below + pref - mine;                    // units before this thread's sequences
     __syncthreads();
-    const int id = id0 + (SOLO ? warp : 0);
-    const int wk = SOLO ? warp : 0;
-    if (id >= shares || bound[wk] >= bound[wk + 1]) return;       // in a block that shares, all warps alike
-    const long long lo = bound[wk], hi = bound[wk + 1];
+    // Equal shares, the first of them one unit longer where they do not divide; no more shares than units.
+    // A cut within kSnap units of a head's end moves to that end: joining a cut head costs more.
+    const int shares = (int)min((int64_t)(gridDim.x * (SOLO ? W : 1)), max((int64_t)1, total / kLeast));
+    const int id = SOLO ? blockIdx.x * W + warp : blockIdx.x;
+    const int64_t each = quotient(total, shares);
+    const int longer = (int)(total - each * shares);
+    if (total == 0 || id >= shares) return;                       // all warps of a block that shares
     Place<R> at;                                                  // where the share stands
-    at.b = misc[4 * wk]; at.hk = misc[4 * wk + 1]; at.rt = misc[4 * wk + 2]; at.u = misc[4 * wk + 3];
+    int64_t lo, hi;
+    {
+        // lane 0 finds the share's begin, the other lanes its end
+        const int k = id + (lane != 0);
+        const int64_t raw = each * k + min(k, longer);
+        int64_t bound = total;
+        at.b = at.hk = at.rt = at.u = 0;
+        if (raw < total) {
+            int a = 0, z = kThreads;                              // the last thread that starts at or before raw
+            while (z - a > 1) {
+                const int m = (a + z) >> 1;
+                if (starts[m] <= raw) a = m;
+                else z = m;
+            }
+            int64_t in = raw - starts[a], head;
+            at.b = a * per;
+            for (;; ++at.b) {
+                head = units_of_head(seq_of(bt, at.b));
+                if (in < head * p.kvh) break;
+                in -= head * p.kvh;
+            }
+            at.hk = (int)quotient(in, head);
+            in -= head * at.hk;
+            at.load_seq(p);
+            for (;; ++at.rt) {
+                at.load_tile(p);
+                if (in < at.units) break;
+                in -= at.units;
+            }
+            at.u = (int)in;
+            if (at.u <= kSnap) at.u = 0;
+            else if (at.units - at.u <= kSnap) at.u = at.units;
+            bound = raw + (at.u - in);
+        }
+        lo = __shfl_sync(0xffffffffu, bound, 0);
+        hi = __shfl_sync(0xffffffffu, bound, 1);
+        at.b = __shfl_sync(0xffffffffu, at.b, 0);
+        at.hk = __shfl_sync(0xffffffffu, at.hk, 0);
+        at.rt = __shfl_sync(0xffffffffu, at.rt, 0);
+        at.u = __shfl_sync(0xffffffffu, at.u, 0);
+    }
+    if (lo >= hi) return;
     at.load_seq(p);
     at.load_tile(p);
     at.advance(p, 0);
@@ -264,7 +282,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     uint8_t* my_ring = ring + warp * NS * kTile;
     uint64_t* my_bar = bars + warp * NS;
     Place<R> ahead = at;                                          // the next unit to ask for
-    const int share = (int)min(hi - lo, 0x7fffffffll);            // its units
+    const int share = (int)min(hi - lo, (int64_t)0x7fffffff);     // its units
     int left = share - (SOLO ? 0 : warp);                         // of them, from `ahead` on
     if (!SOLO && left > 0) ahead.advance(p, warp);
     int page0 = -1, page1 = -1;
@@ -722,9 +740,12 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
         } else {
             // the head's stretch of the line and the shares whose cuts fall inside it, as the plan above cuts
             constexpr int kSlot = NT * 8 * NG * 32 + 2 * R;
-            const long long head_lo = lo + x - u0;
-            const int c_first = (int)(((head_lo + kSnap + 1) * shares + total - 1) / total) - 1;
-            const int c_last = (int)(((head_lo + at.units - kSnap) * shares + total - 1) / total) - 1;
+            const int64_t head_lo = lo + x - u0;
+            auto share_from = [&](int64_t unit) -> int {          // the first share that begins there or later
+                const int64_t bend = (each + 1) * longer;
+                return unit <= bend ? (int)quotient(unit + each, each + 1) : longer + (int)quotient(unit - bend + each - 1, each);
+            };
+            const int c_first = share_from(head_lo + kSnap + 1) - 1, c_last = share_from(head_lo + at.units - kSnap) - 1;
             bool last = false;
             if (speaks) {
                 float* to = p.part + (size_t)(2 * id + (u0 == 0)) * kSlot;
@@ -747,11 +768,11 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                     if (last) p.tickets[c_first] = 0;             // for the next call
                 }
                 last = __shfl_sync(0xffffffffu, last, 0);
-                if (!SOLO && lane == 0) misc[4 * W] = last;
+                if (!SOLO && lane == 0) *s_last = last;
             }
             if constexpr (!SOLO) {
                 __syncthreads();
-                last = misc[4 * W];
+                last = *s_last;
             }
             if (last) {
                 s.clear();
@@ -812,7 +833,7 @@ template <int NG, int NT, bool SOLO> struct Shape {
     static constexpr int NS = NG == 2 ? 4 : 2;
     static constexpr int MB = SOLO ? (NG == 2 ? 4 : NG == 4 ? 3 : 2) : 1;
     static constexpr size_t smem = (size_t)W * NS * 1280 * NG + join_bytes<NG, W, SOLO>() + (SOLO ? 0 : W * 8 * NT * 8) + W * NS * 8 +
-                                   (2 * W + 1) * 8 + (4 * W + 1) * 4 + 16;
+                                   W * 8 + 32 * W * 8 + 16;
     static_assert(smem <= 227 * 1024 / MB - 1024, "");
     static constexpr int shares = MB * (SOLO ? W : 1);           // of an SM
     static constexpr size_t part_floats = (size_t)2 * shares * (NT * 8 * NG * 32 + 16 * NT);
