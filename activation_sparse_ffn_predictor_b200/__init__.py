@@ -473,6 +473,24 @@ def permute_vector(src, dst, perm, stream=None):
 
 # ---- the dense half of a batched decode block (include/spffn_block.h) -----------------------
 
+_T = None            # torch, once a call of this part has needed it
+_device_now = None   # the current device's index, and a device's current stream as an integer
+_stream_now = None
+
+
+def _torch():
+    global _T, _device_now, _stream_now
+    if _T is None:
+        import torch
+        # the index and the handle themselves where torch has them: the public calls build objects, and a decode
+        # step makes several of these calls for kernels of a few microseconds
+        _device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _stream_now = raw if raw is not None else lambda device: torch.cuda.current_stream(device).cuda_stream
+        _T = torch
+    return _T
+
+
 def _on(device: int, *tensors):
     """Every tensor (None allowed) lives on CUDA device `device`."""
     if device < 0:
@@ -484,19 +502,21 @@ def _on(device: int, *tensors):
 
 def _rows(t, what: str, dtype, T=None, d=None):
     """Row stride of a 2-D tensor whose rows are contiguous; checks its type and shape."""
-    if t.dim() != 2 or (T is not None and t.shape[0] != T) or (d is not None and t.shape[1] != d):
-        raise ValueError("%s: expected shape [%s, %s], got %s" % (what, T, d, tuple(t.shape)))
-    if t.dtype != dtype:
+    shape = t.shape
+    if len(shape) != 2 or (T is not None and shape[0] != T) or (d is not None and shape[1] != d):
+        raise ValueError("%s: expected shape [%s, %s], got %s" % (what, T, d, tuple(shape)))
+    if t.dtype is not dtype:
         raise TypeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise ValueError("%s: rows must be contiguous" % what)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return ld if shape[0] > 1 else shape[1]
 
 
 def _vector(t, what: str, dtype, n: int):
-    if t.dim() != 1 or t.shape[0] != n:
+    if t.shape != (n,):
         raise ValueError("%s: expected shape [%d], got %s" % (what, n, tuple(t.shape)))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
     if n > 1 and t.stride(0) != 1:
         raise ValueError("%s must be contiguous" % what)
@@ -508,12 +528,14 @@ def _ptr(t):
 
 def _call(device: int, stream, name: str, fn, *args):
     """fn(*args, stream) with `device` current; `stream` defaults to that device's current stream."""
-    import torch
-    if torch.cuda.current_device() == device:
-        _check(fn(*args, _stream(stream)), name)
+    handle = _stream_now(device) if stream is None else getattr(stream, "cuda_stream", stream)
+    if _device_now() == device:
+        status = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)), name)
+        with _T.cuda.device(device):
+            status = fn(*args, handle)
+    if status != OK:
+        _check(status, name)
 
 
 def norm_quant(x, y, g, x_out, q, scale, eps: float = 1e-6, stream=None):
@@ -521,7 +543,7 @@ def norm_quant(x, y, g, x_out, q, scale, eps: float = 1e-6, stream=None):
     storage type, ``q [T, d]`` int8 and ``scale [T]`` fp32 with ``q scale`` the normalised row times ``g``.
     ``x [T, d]`` float16 or bfloat16; ``y [T, d]`` of that type, float32 or None; ``g [d]`` or None; ``x_out``
     may be ``x`` (or ``y`` of the same type) or None."""
-    import torch
+    torch = _torch()
     T, d = x.shape
     code, dev = _dtype_code(x), x.get_device()
     ldx = _rows(x, "x", x.dtype)
@@ -533,21 +555,21 @@ def norm_quant(x, y, g, x_out, q, scale, eps: float = 1e-6, stream=None):
     if g is not None:
         _vector(g, "g", x.dtype, d)
     _on(dev, x, y, g, x_out, q, scale)
-    _call(dev, stream, "spffn_norm_quant", library().spffn_norm_quant, T, d, code, x.data_ptr(), ldx, _ptr(y), ldy,
+    _call(dev, stream, "spffn_norm_quant", _lib.spffn_norm_quant if _lib is not None else library().spffn_norm_quant, T, d, code, x.data_ptr(), ldx, _ptr(y), ldy,
           y_f32, _ptr(g), eps, _ptr(x_out), ldo, q.data_ptr(), ldq, scale.data_ptr())
 
 
 def quantize_rows(x, q, scale, stream=None):
     """8-bit rows with a scale each (spffn_quantize_rows): ``x [T, d]`` float16, bfloat16 or float32 to
     ``q [T, d]`` int8 and ``scale [T]`` fp32.  Weights ``[N, K]`` get their scales per channel this way."""
-    import torch
+    torch = _torch()
     T, d = x.shape
     f32 = x.dtype == torch.float32
     code, dev = F16 if f32 else _dtype_code(x), x.get_device()
     ldx, ldq = _rows(x, "x", x.dtype), _rows(q, "q", torch.int8, T, d)
     _vector(scale, "scale", torch.float32, T)
     _on(dev, x, q, scale)
-    _call(dev, stream, "spffn_quantize_rows", library().spffn_quantize_rows, T, d, code, x.data_ptr(), ldx, f32,
+    _call(dev, stream, "spffn_quantize_rows", _lib.spffn_quantize_rows if _lib is not None else library().spffn_quantize_rows, T, d, code, x.data_ptr(), ldx, f32,
           q.data_ptr(), ldq, scale.data_ptr())
 
 
@@ -560,7 +582,7 @@ class Linear8:
     """
 
     def __init__(self, W, w_scale, bias=None, max_tokens: int = 256, dtype=None, workspace=None):
-        import torch
+        torch = _torch()
         self.out_dtype = dtype if dtype is not None else bias.dtype if bias is not None else torch.float16
         self.N, self.K = (int(v) for v in W.shape)
         self.max_tokens = int(max_tokens)
@@ -602,12 +624,12 @@ class Linear8:
 
     def forward(self, q, scale, y, stream=None):
         """``q [T, K]`` int8 and ``scale [T]`` fp32 (as norm_quant leaves them) to ``y [T, N]``."""
-        import torch
+        torch = _torch()
         T = q.shape[0]
         ldq, ldy = _rows(q, "q", torch.int8, T, self.K), _rows(y, "y", self.out_dtype, T, self.N)
         _vector(scale, "scale", torch.float32, T)
         _on(self.device, q, scale, y)
-        _call(self.device, stream, "spffn_mm8_forward", library().spffn_mm8_forward, self.ctx, q.data_ptr(), ldq,
+        _call(self.device, stream, "spffn_mm8_forward", _lib.spffn_mm8_forward, self.ctx, q.data_ptr(), ldq,
               scale.data_ptr(), T, y.data_ptr(), ldy)
 
     def last_device_error(self, stream=None):
@@ -636,7 +658,7 @@ class Rope:
     from rope_frequencies), pairs ``(2i, 2i + 1)`` if ``interleaved`` else ``(i, i + dim / 2)`` of the first dim dims."""
 
     def __init__(self, freqs, interleaved: bool = False, amplitude: float = 1.0):
-        import torch
+        torch = _torch()
         self.freqs = torch.from_numpy(np.ascontiguousarray(freqs, dtype=np.float64)).cuda() if isinstance(freqs, np.ndarray) else freqs
         _vector(self.freqs, "freqs", torch.float64, self.freqs.numel())
         self.interleaved, self.amplitude = bool(interleaved), float(amplitude)
@@ -653,7 +675,7 @@ class KvCache4:
 
     def __init__(self, pages: int, page_size: int, nh: int, kvh: int, dh: int, dtype, max_seqs: int, max_tokens: int,
                  rope: Optional[Rope] = None, pool=None, workspace=None, device=None):
-        import torch
+        torch = _torch()
         code = {torch.float16: F16, torch.bfloat16: BF16}.get(dtype)
         if code is None:
             raise TypeError("dtype must be float16 or bfloat16, got %s" % dtype)
@@ -694,17 +716,18 @@ class KvCache4:
 
     def _heads(self, t, what: str, T: int, heads: int):
         """Row stride of [T, heads, dh] (or [T, heads * dh]) whose rows are contiguous."""
-        if t.dim() == 3:
-            if t.shape != (T, heads, self.dh) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.dh):
+        if len(t.shape) == 3:
+            ld, head, one = t.stride()
+            if t.shape != (T, heads, self.dh) or one != 1 or (heads > 1 and head != self.dh):
                 raise ValueError("%s: expected [%d, %d, %d] with contiguous rows, got %s, strides %s" % (
                     what, T, heads, self.dh, tuple(t.shape), t.stride()))
-            if t.dtype != self.dtype:
+            if t.dtype is not self.dtype:
                 raise TypeError("%s: expected %s, got %s" % (what, self.dtype, t.dtype))
-            return t.stride(0) if T > 1 else heads * self.dh
+            return ld if T > 1 else heads * self.dh
         return _rows(t, what, self.dtype, T, heads * self.dh)
 
     def _batch(self, table, lens, start):
-        import torch
+        torch = _torch()
         B = lens.shape[0]
         ldt = _rows(table, "table", torch.int32, B)
         _vector(lens, "lens", torch.int32, B)
@@ -716,6 +739,7 @@ class KvCache4:
     def append(self, q, k, v, table, lens, start=None, q_out=None, stream=None):
         """Rotate ``q [T, nh, dh]`` into ``q_out`` (may be ``q``; both None to leave it out) and append ``k, v
         [T, kvh, dh]``, k rotated, at their sequences' positions."""
+        _torch()
         T = k.shape[0]
         ldk, ldv = self._heads(k, "k", T, self.kvh), self._heads(v, "v", T, self.kvh)
         ldq, ldo = (0, 0) if q is None else (self._heads(q, "q", T, self.nh), 0)
@@ -723,22 +747,23 @@ class KvCache4:
             ldo = self._heads(q_out, "q_out", T, self.nh)
         batch = self._batch(table, lens, start)
         _on(self.device, q, k, v, q_out)
-        _call(self.device, stream, "spffn_kv4_append", library().spffn_kv4_append, self.ctx, _ptr(q), ldq, k.data_ptr(),
+        _call(self.device, stream, "spffn_kv4_append", _lib.spffn_kv4_append, self.ctx, _ptr(q), ldq, k.data_ptr(),
               ldk, v.data_ptr(), ldv, T, *batch, _ptr(q_out), ldo)
 
     def attend(self, q, table, lens, start=None, out=None, scale: Optional[float] = None, stream=None):
         """Attention of the new tokens' ``q [T, nh, dh]`` over their sequences' cached positions up to their own, into
         ``out [T, nh, dh]``; ``scale`` defaults to 1 / sqrt(dh)."""
+        _torch()
         T = q.shape[0]
         ldq, ldo = self._heads(q, "q", T, self.nh), self._heads(out, "out", T, self.nh)
         batch = self._batch(table, lens, start)
         _on(self.device, q, out)
-        _call(self.device, stream, "spffn_kv4_attend", library().spffn_kv4_attend, self.ctx, q.data_ptr(), ldq, T, *batch,
+        _call(self.device, stream, "spffn_kv4_attend", _lib.spffn_kv4_attend, self.ctx, q.data_ptr(), ldq, T, *batch,
               self.dh ** -0.5 if scale is None else scale, out.data_ptr(), ldo)
 
     def read(self, pages, K, V, stream=None):
         """The cached values of ``pages [n]`` (int32) into ``K, V [n, page_size, kvh, dh]``."""
-        import torch
+        torch = _torch()
         n = pages.shape[0]
         _vector(pages, "pages", torch.int32, n)
         for t, what in ((K, "K"), (V, "V")):
@@ -747,7 +772,7 @@ class KvCache4:
             if t.dtype != self.dtype:
                 raise TypeError("%s: expected %s, got %s" % (what, self.dtype, t.dtype))
         _on(self.device, pages, K, V)
-        _call(self.device, stream, "spffn_kv4_read", library().spffn_kv4_read, self.ctx, pages.data_ptr(), n, K.data_ptr(),
+        _call(self.device, stream, "spffn_kv4_read", _lib.spffn_kv4_read, self.ctx, pages.data_ptr(), n, K.data_ptr(),
               V.data_ptr())
 
     def last_device_error(self, stream=None):

@@ -15,7 +15,7 @@ struct AppendParams {
     uint8_t* pool;
     const double* freqs;
     float amp;
-    int nh, kvh, dh, rd, inter;
+    int nh, kvh, rd, inter;
     Batch b;
 };
 
@@ -34,62 +34,105 @@ __device__ __forceinline__ float f16_value(float v) {      // rounded to fp16, k
     return __half2float(__float2half_rn(fminf(fmaxf(v, -65504.f), 65504.f)));
 }
 
-// One CTA per (row, slice of its heads); 8 dims of a head per thread, so a group of 32 dims
-// is four neighbouring lanes.
-template <typename T>
+// cosine and sine of pos freq: the turns in fp64 (a far position keeps its angle to 2^-53 of the turns), the
+// fraction of a turn as a high and a low fp32 part, the low one by the first term of its series
+__device__ __forceinline__ void angle(int pos, double freq, float amp, float* co, float* si) {
+    double t = (double)pos * freq * 0.15915494309189535;          // 1 / (2 pi)
+    t = 2.0 * (t - rint(t));
+    const float hi = (float)t, lo = (float)(t - (double)hi) * 3.14159265f;
+    float s, c;
+    sincospif(hi, &s, &c);
+    *co = amp * fmaf(-s, lo, c);
+    *si = amp * fmaf(c, lo, s);
+}
+
+// A block takes a row, or a slice of its heads where there are few rows; a thread 8 dims of a head, so a
+// group of 32 dims is four neighbouring lanes and a head 4 NG.  VEC: rows in 16-byte pieces and rotated pairs
+// in whole pieces; otherwise element by element.
+// Bound by the bytes of q, k and v at many rows, by latency at few.  V codes go out as words put together
+// from two groups' lanes: a head's V codes lie in 8 places, and single halfwords doubled the stores.
+template <typename T, int NG, bool VEC>
 __global__ void __launch_bounds__(256) k_append(const AppendParams p) {
-    __shared__ float cs[128], sn[128];
+    using L = Blk<NG>;
+    constexpr int LH = 4 * NG, DH = 32 * NG;                      // lanes of a head
+    __shared__ float cs[DH / 2], sn[DH / 2];
     const int t = blockIdx.x;
     const int s = seq_of_row(p.b, t);
     if (s < 0) return;
     const Seq sq = seq_of(p.b, s);
     if (!sq.ok || t < sq.row0 || t >= sq.row0 + sq.n) return;
     const int pos = sq.len - sq.n + (t - sq.row0);
+    const int page = p.b.table[(int64_t)s * p.b.ldt + (pos >> p.b.page_log)];
     const int hrd = p.rd >> 1;
-    for (int i = threadIdx.x; i < hrd; i += blockDim.x) {
-        double a = (double)pos * p.freqs[i], si, co;
-        sincos(a, &si, &co);
-        cs[i] = (float)(co * (double)p.amp);
-        sn[i] = (float)(si * (double)p.amp);
-    }
-    __syncthreads();
-    const int page = p.b.table[(int64_t)s * p.b.ldt + pos / p.b.page];
-    const bool paged = page >= 0 && page < p.b.pages;
+    for (int i = threadIdx.x; i < hrd; i += blockDim.x) angle(pos, p.freqs[i], p.amp, &cs[i], &sn[i]);
+    if (hrd) __syncthreads();
+    const bool paged = (unsigned)page < (unsigned)p.b.pages;
     if (!paged && threadIdx.x == 0 && blockIdx.y == 0) latch(p.b.err, ERR_PAGE_RANGE);
-    const int vph = p.dh >> 3, ng = p.dh >> 5;              // pieces of 8 dims and groups of a head
-    const int heads = (p.q ? p.nh : 0) + 2 * p.kvh, q_heads = p.q ? p.nh : 0;
-    const int tok = pos % p.b.page, blk = tok >> 4;
-    const int items = heads * vph;
+    const int q_heads = p.q ? p.nh : 0, heads = q_heads + 2 * p.kvh;
+    const int tok = pos & (p.b.page - 1), lt = tok & 15;
+    uint8_t* rec0 = p.pool + ((int64_t)page * p.kvh * (p.b.page >> 4) + (tok >> 4)) * L::kBytes;
+    const int64_t head_bytes = (int64_t)(p.b.page >> 4) * L::kBytes;
+    const int items = heads * LH, lane = threadIdx.x & 31;
     // whole warps go round together: lanes past the end repeat the last item and store nothing
     for (int it0 = blockIdx.y * blockDim.x + (threadIdx.x & ~31); it0 < items; it0 += gridDim.y * blockDim.x) {
-        const bool live = it0 + (threadIdx.x & 31) < items;
-        const int it = live ? it0 + (threadIdx.x & 31) : items - 1;
-        const int h = it / vph, e0 = (it % vph) * 8;
+        const bool live = it0 + lane < items;
+        const int it = live ? it0 + lane : items - 1;
+        const int h = it / LH, j = it % LH, e0 = 8 * j;
         const int kind = h < q_heads ? 0 : h < q_heads + p.kvh ? 1 : 2;
         const int hh = kind == 0 ? h : kind == 1 ? h - q_heads : h - q_heads - p.kvh;
-        const T* x = kind == 0 ? static_cast<const T*>(p.q) + t * p.ldq
-                               : kind == 1 ? static_cast<const T*>(p.k) + t * p.ldk : static_cast<const T*>(p.v) + t * p.ldv;
-        x += (int64_t)hh * p.dh;
+        const T* x = (kind == 0 ? static_cast<const T*>(p.q) + t * p.ldq
+                                : kind == 1 ? static_cast<const T*>(p.k) + t * p.ldk : static_cast<const T*>(p.v) + t * p.ldv) + (int64_t)hh * DH;
         float v[8];
+        if constexpr (VEC) {
+            unpack8<T>(*reinterpret_cast<const uint4*>(x + e0), v);
+            if (kind < 2 && e0 < p.rd) {
+                if (p.inter) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = e0 + i;
-            float a = DT<T>::f(x[e]);
-            if (kind < 2 && e < p.rd) {
-                const int f = p.inter ? e >> 1 : e < hrd ? e : e - hrd;
-                const bool second = p.inter ? e & 1 : e >= hrd;
-                const float o = DT<T>::f(x[p.inter ? e ^ 1 : second ? e - hrd : e + hrd]);
-                a = second ? __fadd_rn(__fmul_rn(a, cs[f]), __fmul_rn(o, sn[f]))
-                           : __fsub_rn(__fmul_rn(a, cs[f]), __fmul_rn(o, sn[f]));
+                    for (int i = 0; i < 8; i += 2) {
+                        const float co = cs[(e0 + i) >> 1], si = sn[(e0 + i) >> 1], a = v[i], b = v[i + 1];
+                        v[i] = __fsub_rn(__fmul_rn(a, co), __fmul_rn(b, si));
+                        v[i + 1] = __fadd_rn(__fmul_rn(b, co), __fmul_rn(a, si));
+                    }
+                } else {
+                    const bool second = e0 >= hrd;
+                    const int f0 = second ? e0 - hrd : e0;
+                    float o[8];
+                    unpack8<T>(*reinterpret_cast<const uint4*>(x + (second ? f0 : e0 + hrd)), o);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float m = __fmul_rn(v[i], cs[f0 + i]), n = __fmul_rn(o[i], sn[f0 + i]);
+                        v[i] = second ? __fadd_rn(m, n) : __fsub_rn(m, n);
+                    }
+                }
             }
-            v[i] = a;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = e0 + i;
+                float a = DT<T>::f(x[e]);
+                if (kind < 2 && e < p.rd) {
+                    const int f = p.inter ? e >> 1 : e < hrd ? e : e - hrd;
+                    const bool second = p.inter ? e & 1 : e >= hrd;
+                    const float o = DT<T>::f(x[p.inter ? e ^ 1 : second ? e - hrd : e + hrd]);
+                    const float m = __fmul_rn(a, cs[f]), n = __fmul_rn(o, sn[f]);
+                    a = second ? __fadd_rn(m, n) : __fsub_rn(m, n);
+                }
+                v[i] = a;
+            }
         }
         __syncwarp();        // q_out may be q: the loads of a head's lanes (one warp) come before the stores
         if (kind == 0 && live) {
-            T* o = static_cast<T*>(p.q_out) + t * p.ldqo + (int64_t)hh * p.dh + e0;
+            T* o = static_cast<T*>(p.q_out) + t * p.ldqo + (int64_t)hh * DH + e0;
+            T w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = DT<T>::r(v[i]);
+            for (int i = 0; i < 8; ++i) w[i] = DT<T>::r(v[i]);
+            if constexpr (VEC) *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(w);
+            else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = w[i];
+            }
         }
+        if (__all_sync(0xffffffffu, kind == 0)) continue;
         float lo = v[0], hi = v[0], bad = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -105,56 +148,63 @@ __global__ void __launch_bounds__(256) k_append(const AppendParams p) {
         }
         const float zero = f16_value(lo), step = bad == 0.f ? f16_value(__fdiv_rn(__fsub_rn(hi, lo), 15.f)) : __int_as_float(0x7fc00000);
         const uint32_t w = pack8(v, step, zero);
+        // lane j's word of the V codes: place r = j / (NG / 2), groups 2 (j % (NG / 2)) and the next
+        const int r = j / (NG / 2), g2 = 2 * (j % (NG / 2)), from = (lane & ~(LH - 1)) + 4 * g2 + (r >> 1);
+        const uint32_t va = __shfl_sync(0xffffffffu, w, from), vb = __shfl_sync(0xffffffffu, w, from + 4);
         if (!paged || !live || kind == 0) continue;
-        const int g = e0 >> 5, c = (e0 & 31) >> 3, lt = tok & 15;
-        uint8_t* rec = p.pool + (((int64_t)page * p.kvh + hh) * (p.b.page >> 4) + blk) * (640 * ng);
-        auto put = [&](auto tag) {
-            using L = Blk<decltype(tag)::value>;
-            if (kind == 1) *reinterpret_cast<uint32_t*>(rec + L::k(lt, g, c)) = w;
-            else {
-                *reinterpret_cast<uint16_t*>(rec + L::v(lt, g, 2 * c)) = (uint16_t)w;
-                *reinterpret_cast<uint16_t*>(rec + L::v(lt, g, 2 * c + 1)) = (uint16_t)(w >> 16);
-            }
-            if (c == 0) {
-                *reinterpret_cast<__half*>(rec + (kind == 1 ? L::ks(lt, g) : L::vs(lt, g))) = __float2half_rn(step);
-                *reinterpret_cast<__half*>(rec + (kind == 1 ? L::kz(lt, g) : L::vz(lt, g))) = __float2half_rn(zero);
-            }
-        };
-        if (ng == 2) put(std::integral_constant<int, 2>());
-        else if (ng == 4) put(std::integral_constant<int, 4>());
-        else put(std::integral_constant<int, 8>());
+        const int g = j >> 2, c = j & 3;
+        uint8_t* rec = rec0 + hh * head_bytes;
+        if (kind == 1) *reinterpret_cast<uint32_t*>(rec + L::k(lt, g, c)) = w;
+        else *reinterpret_cast<uint32_t*>(rec + L::v(lt, g2, r)) = __byte_perm(va, vb, r & 1 ? 0x7632 : 0x5410);
+        if (c == 0) {
+            *reinterpret_cast<__half*>(rec + (kind == 1 ? L::ks(lt, g) : L::vs(lt, g))) = __float2half_rn(step);
+            *reinterpret_cast<__half*>(rec + (kind == 1 ? L::kz(lt, g) : L::vz(lt, g))) = __float2half_rn(zero);
+        }
     }
 }
 
-// 8 values of one (page of the list, kv head, token) per thread
+// A warp takes a block of 16 tokens of one kv head: the block comes into shared memory as it lies, the values go
+// out a head's row at a time.  Bound by the bytes written (16 bits a value for 5 read).
 template <typename T, int NG>
-__global__ void __launch_bounds__(256) k_read(const uint8_t* pool, const int32_t* ids, int64_t items, int kvh, int page,
+__global__ void __launch_bounds__(256) k_read(const uint8_t* pool, const int32_t* ids, int64_t blocks, int kvh, int page_log,
                                               int pages, T* K, T* V, uint32_t* err) {
     using L = Blk<NG>;
-    const int64_t it = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (it >= items) return;
-    const int e0 = (int)(it % (4 * NG)) * 8, tok = (int)(it / (4 * NG) / kvh % page), h = (int)(it / (4 * NG) % kvh);
-    const int64_t i = it / (4 * NG) / kvh / page;
+    constexpr int LH = 4 * NG, TW = 32 / LH;                      // lanes of a row, rows of a warp at a time
+    __shared__ __align__(16) uint8_t buf[8][L::kBytes];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t it = (int64_t)blockIdx.x * 8 + warp;            // (entry of the list, block of the page, kv head)
+    if (it >= blocks) return;
+    const int h = (int)(it % kvh), blk = (int)(it / kvh) & ((1 << (page_log - 4)) - 1);
+    const int64_t i = (it / kvh) >> (page_log - 4);
     const int id = ids[i];
-    if (id < 0 || id >= pages) {
-        if (e0 == 0) latch(err, ERR_PAGE_RANGE);
+    if ((unsigned)id >= (unsigned)pages) {
+        if (lane == 0) latch(err, ERR_PAGE_RANGE);
         return;
     }
-    const uint8_t* rec = pool + (((int64_t)id * kvh + h) * (page >> 4) + (tok >> 4)) * L::kBytes;
-    const int lt = tok & 15, g = e0 >> 5, c = (e0 & 31) >> 3;
-    auto half_at = [&](int o) { return __half2float(*reinterpret_cast<const __half*>(rec + o)); };
-    const uint32_t kw = *reinterpret_cast<const uint32_t*>(rec + L::k(lt, g, c));
-    const uint32_t vw = *reinterpret_cast<const uint16_t*>(rec + L::v(lt, g, 2 * c)) |
-                        ((uint32_t)*reinterpret_cast<const uint16_t*>(rec + L::v(lt, g, 2 * c + 1)) << 16);
-    const float ks = half_at(L::ks(lt, g)), kz = half_at(L::kz(lt, g)), vs = half_at(L::vs(lt, g)), vz = half_at(L::vz(lt, g));
-    T ko[8], vo[8];
+    const uint4* src = reinterpret_cast<const uint4*>(pool + ((((int64_t)id * kvh + h) << (page_log - 4)) + blk) * L::kBytes);
+    uint8_t* rec = buf[warp];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        ko[j] = DT<T>::r(fmaf((float)((kw >> (4 * j)) & 15u), ks, kz));
-        vo[j] = DT<T>::r(fmaf((float)((vw >> (4 * j)) & 15u), vs, vz));
+    for (int k = 0; k < (L::kBytes / 16 + 31) / 32; ++k)
+        if (k * 32 + lane < L::kBytes / 16) reinterpret_cast<uint4*>(rec)[k * 32 + lane] = __ldg(src + k * 32 + lane);
+    __syncwarp();
+    const int j = lane % LH, g = j >> 2, c = j & 3;
+    auto half_at = [&](int o) { return __half2float(*reinterpret_cast<const __half*>(rec + o)); };
+#pragma unroll 4
+    for (int lt = lane / LH; lt < 16; lt += TW) {
+        const uint32_t kw = *reinterpret_cast<const uint32_t*>(rec + L::k(lt, g, c));
+        const uint32_t vw = *reinterpret_cast<const uint16_t*>(rec + L::v(lt, g, 2 * c)) |
+                            ((uint32_t)*reinterpret_cast<const uint16_t*>(rec + L::v(lt, g, 2 * c + 1)) << 16);
+        const float ks = half_at(L::ks(lt, g)), kz = half_at(L::kz(lt, g)), vs = half_at(L::vs(lt, g)), vz = half_at(L::vz(lt, g));
+        T ko[8], vo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            ko[e] = DT<T>::r(fmaf((float)((kw >> (4 * e)) & 15u), ks, kz));
+            vo[e] = DT<T>::r(fmaf((float)((vw >> (4 * e)) & 15u), vs, vz));
+        }
+        const int64_t at = ((((i << page_log) + blk * 16 + lt) * kvh + h) * LH + j) * 8;
+        *reinterpret_cast<uint4*>(K + at) = *reinterpret_cast<const uint4*>(ko);
+        *reinterpret_cast<uint4*>(V + at) = *reinterpret_cast<const uint4*>(vo);
     }
-    *reinterpret_cast<uint4*>(K + it * 8) = *reinterpret_cast<const uint4*>(ko);
-    *reinterpret_cast<uint4*>(V + it * 8) = *reinterpret_cast<const uint4*>(vo);
 }
 
 bool valid(const spffn_kv4_config* c) {
@@ -273,12 +323,26 @@ spffn_status spffn_kv4_append(spffn_kv4_ctx* ctx, const void* q, int64_t ldq, co
     if (!aligned_to(q, 2) || !aligned_to(k, 2) || !aligned_to(v, 2) || !aligned_to(q_out, 2)) return SPFFN_ERR_INVALID_ARG;
     if (q && q == q_out && ldq != ldqo) return SPFFN_ERR_INVALID_ARG;
     if (!on_device(ctx->device)) return SPFFN_ERR_INVALID_ARG;
-    AppendParams p{q, k, v, q_out, ldq, ldk, ldv, ldqo, ctx->pool, ctx->freqs, c.rope_amplitude, c.nh, c.kvh, c.dh,
+    AppendParams p{q, k, v, q_out, ldq, ldk, ldv, ldqo, ctx->pool, ctx->freqs, c.rope_amplitude, c.nh, c.kvh,
                    c.rope_dim, c.rope_interleaved != 0, batch_of(ctx, T, table, ld_table, width, lens, q_start, B)};
+    // slices of a row where the rows alone do not fill the device (8 blocks an SM, two rounds)
     const int items = ((q ? c.nh : 0) + 2 * c.kvh) * (c.dh / 8);
-    const dim3 grid(T, std::max(1, std::min(65535, (items + 1023) / 1024)));
-    if (c.dtype == SPFFN_BF16) k_append<__nv_bfloat16><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
-    else k_append<__half><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
+    const dim3 grid(T, std::max(1, std::min((items + 255) / 256, 16 * ctx->sms / T)));
+    auto row16 = [](const void* x, int64_t ld) { return aligned_to(x, 16) && ld % 8 == 0; };
+    const bool vec = row16(q, ldq) && row16(q_out, ldqo) && row16(k, ldk) && row16(v, ldv) && c.rope_dim % (c.rope_interleaved ? 8 : 16) == 0;
+    cudaStream_t st = (cudaStream_t)stream;
+    auto go = [&](auto tag, auto ng) {
+        using T_ = decltype(tag);
+        if (vec) k_append<T_, decltype(ng)::value, true><<<grid, 256, 0, st>>>(p);
+        else k_append<T_, decltype(ng)::value, false><<<grid, 256, 0, st>>>(p);
+    };
+    auto by_ng = [&](auto tag) {
+        if (c.dh == 64) go(tag, std::integral_constant<int, 2>());
+        else if (c.dh == 128) go(tag, std::integral_constant<int, 4>());
+        else go(tag, std::integral_constant<int, 8>());
+    };
+    if (c.dtype == SPFFN_BF16) by_ng(__nv_bfloat16());
+    else by_ng(__half());
     return record_cuda(cudaGetLastError());
 }
 
@@ -301,13 +365,15 @@ spffn_status spffn_kv4_read(spffn_kv4_ctx* ctx, const int32_t* page_ids, int32_t
     if (!page_ids || !K || !V || K == V || !aligned_to(page_ids, 4) || !aligned_to(K, 16) || !aligned_to(V, 16)) return SPFFN_ERR_INVALID_ARG;
     if (!on_device(ctx->device)) return SPFFN_ERR_INVALID_ARG;
     const auto& c = ctx->cfg;
-    const int64_t items = (int64_t)n * c.page_size * c.kvh * (c.dh / 8);
-    if ((items + 255) / 256 > 0x7fffffffLL) return SPFFN_ERR_INVALID_ARG;
-    const unsigned grid = (unsigned)((items + 255) / 256);
+    const int64_t blocks = (int64_t)n * (c.page_size / 16) * c.kvh;
+    if ((blocks + 7) / 8 > 0x7fffffffLL) return SPFFN_ERR_INVALID_ARG;
+    const unsigned grid = (unsigned)((blocks + 7) / 8);
+    int page_log = 4;
+    while ((1 << page_log) < c.page_size) ++page_log;
     cudaStream_t st = (cudaStream_t)stream;
     auto go = [&](auto tag, auto ng) {
         using T = decltype(tag);
-        k_read<T, decltype(ng)::value><<<grid, 256, 0, st>>>(ctx->pool, page_ids, items, c.kvh, c.page_size, c.pages,
+        k_read<T, decltype(ng)::value><<<grid, 256, 0, st>>>(ctx->pool, page_ids, blocks, c.kvh, page_log, c.pages,
                                                              static_cast<T*>(K), static_cast<T*>(V), ctx->err());
     };
     auto by_ng = [&](auto tag) {

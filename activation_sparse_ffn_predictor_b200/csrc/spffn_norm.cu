@@ -91,13 +91,115 @@ __global__ void __launch_bounds__(256) k_norm_any(const NParams p) {
     }
 }
 
-template <typename X, typename Y, typename T, bool NORM>
-cudaError_t launch(const NParams& p, cudaStream_t st) {
-    k_norm_any<X, Y, T, NORM><<<p.T, 256, 0, st>>>(p);
-    return cudaGetLastError();
+// The wide path: rows in pieces of 8 elements (16-byte loads of the storage type), the row in registers
+// between its two passes, so that memory sees every byte once.  NT threads a row, at most 4 pieces a
+// thread; a row of up to 1024 elements is one warp's, eight rows a block.
+template <typename X> __device__ __forceinline__ void load8(const X* p, float* f) {
+    if constexpr (sizeof(X) == 4) {
+        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    } else {
+        unpack8<X>(*reinterpret_cast<const uint4*>(p), f);
+    }
 }
 
-template <typename T> bool elem_aligned(const void* p) { return aligned_to(p, sizeof(T)); }
+template <typename X, typename Y, typename T, bool NORM, int NT>
+__global__ void __launch_bounds__(NT == 32 ? 256 : NT) k_norm_wide(const NParams p) {
+    constexpr int V = 4;
+    __shared__ float2 red[NT / 32];
+    const int64_t t = NT == 32 ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+    if (t >= p.T) return;                                  // whole warps, in the one-warp form only
+    const int i0 = NT == 32 ? threadIdx.x & 31 : threadIdx.x, pieces = p.d >> 3;
+    const X* x = static_cast<const X*>(p.x) + t * p.ldx;
+    const Y* y = static_cast<const Y*>(p.y) + t * p.ldy;
+    const T* g = static_cast<const T*>(p.g);
+    float u[V][8], ss = 0.f, a = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int i = i0 + v * NT;
+        if (i >= pieces) continue;
+        load8(x + 8 * i, u[v]);
+        if (NORM && p.y) {
+            float o[8];
+            load8(y + 8 * i, o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[v][k] = __fadd_rn(u[v][k], o[k]);
+        }
+    }
+    if (NORM && p.x_out) {
+        T* xo = static_cast<T*>(p.x_out) + t * p.ldo;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int i = i0 + v * NT;
+            if (i >= pieces) continue;
+            T o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = DT<T>::r(u[v][k]);
+            *reinterpret_cast<uint4*>(xo + 8 * i) = *reinterpret_cast<const uint4*>(o);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int i = i0 + v * NT;
+        if (i >= pieces) continue;
+        if (NORM) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) ss += u[v][k] * u[v][k];
+            if (g) {
+                float gv[8];
+                load8(g + 8 * i, gv);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) u[v][k] = __fmul_rn(u[v][k], gv[k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) ss += u[v][k] * 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a = fmaxf(a, fabsf(u[v][k]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    }
+    if constexpr (NT > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(ss, a);
+        __syncthreads();
+        ss = 0.f;
+        a = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            ss += red[w].x;
+            a = fmaxf(a, red[w].y);
+        }
+    }
+    float scale;
+    const float r = row_factor<NORM>(ss, a, p.d, p.eps, &scale);
+    if (i0 == 0) p.scale[t] = scale;
+    int8_t* q = p.q + t * p.ldq;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int i = i0 + v * NT;
+        if (i >= pieces) continue;
+        uint32_t b[2] = {0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) b[k >> 2] |= ((uint32_t)to_q(u[v][k], r) & 255u) << (8 * (k & 3));
+        *reinterpret_cast<uint2*>(q + 8 * i) = make_uint2(b[0], b[1]);
+    }
+}
+
+template <typename X, typename Y, typename T, bool NORM>
+cudaError_t launch(const NParams& p, cudaStream_t st) {
+    const bool wide = p.d % 8 == 0 && p.d <= 16384 && aligned_to(p.x, 16) && p.ldx % 8 == 0 && aligned_to(p.y, 16) && p.ldy % 8 == 0 &&
+                      aligned_to(p.g, 16) && aligned_to(p.x_out, 16) && p.ldo % 8 == 0 && aligned_to(p.q, 8) && p.ldq % 8 == 0;
+    if (!wide) k_norm_any<X, Y, T, NORM><<<p.T, 256, 0, st>>>(p);
+    else if (p.d <= 1024) k_norm_wide<X, Y, T, NORM, 32><<<(p.T + 7) / 8, 256, 0, st>>>(p);
+    else if (p.d <= 4096) k_norm_wide<X, Y, T, NORM, 128><<<p.T, 128, 0, st>>>(p);
+    else if (p.d <= 8192) k_norm_wide<X, Y, T, NORM, 256><<<p.T, 256, 0, st>>>(p);
+    else k_norm_wide<X, Y, T, NORM, 512><<<p.T, 512, 0, st>>>(p);
+    return cudaGetLastError();
+}
 
 }  // namespace
 }  // namespace spffn
