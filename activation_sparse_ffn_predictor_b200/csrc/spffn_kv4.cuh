@@ -68,7 +68,7 @@ __device__ __forceinline__ int seq_of_row(const Batch& b, int t) {
 }
 
 struct Layout {
-    size_t ctl, tickets, part, total;
+    size_t ctl, meta, part, total;
 };
 
 }  // namespace kv4

@@ -19,13 +19,13 @@
 // that p s stays in fp16's range.
 //
 // Work: a unit is 32 positions of one (sequence, kv head, tile of query rows).  The units of the
-// batch are one line, cut into equal shares, one a warp or one a block; they are found from the lengths
-// on the device (a captured graph replays with other lengths).  In a block's share the units go round
-// the warps; each warp streams its own through a ring of bulk copies (a unit is one stretch of a page,
-// two where pages have 16 tokens) and nothing waits for another warp until a head's end, where
-// the warps' states are joined through shared memory.  A head that several shares cut leaves its
-// states in the workspace; the last to arrive joins them in their order, so the result does not
-// depend on which it is.
+// batch are one line, cut into equal shares, one a warp, which finds it from the lengths on the device (a
+// captured graph replays with other lengths) and streams its units through a ring of bulk copies of its
+// own (a unit is one stretch of a page, two where pages have 16 tokens): no warp waits for another.
+// A head that lies inside a share is written out at once; the parts of a cut one go to the workspace and
+// k_join adds them in their order.  (Measured and not kept: half shares that warps take as they come,
+// 137 us against 127 at 32 sequences of 1400 positions, 72 heads; blocks that go through a share together
+// and join through shared memory, with the last block to arrive joining the cut heads, 156 us.)
 #include "spffn_umma.cuh"
 #include "spffn_kv4.cuh"
 
@@ -39,18 +39,16 @@ using um::ub_expect;
 using um::ub_init;
 using um::ub_try;
 
-#ifndef SOLO_MIN
-#define SOLO_MIN 200
-#endif
 constexpr int kUnit = 32;             // positions of a unit
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct KParams {
     AttendArgs a;
     const uint8_t* pool;
-    float* part;                      // [2 shares][slot floats]
-    uint32_t* tickets;                // [shares]
+    float* part;                      // [2 shares][R rows][dh], then [2 shares][R] exponents and sums
+    uint2* meta;                      // [T][nh] the shares that a row is cut into (and its place in its tile)
     int nh, kvh, G;
+    int many;                         // the most shares
     int qvec, ovec;                   // rows of q in 16-byte pieces, rows of out in 8-byte pieces
     uint32_t head_bytes, page_bytes;  // of one kv head of a page, and of a page
 };
@@ -171,91 +169,94 @@ template <int NG, int NT> struct State {
     }
 };
 
-template <int NG, int W, bool SOLO> constexpr int join_bytes() { return SOLO ? 0 : W / 2 * 8 * NG * 32 * 4; }  // 8 rows of half the warps' states
+__device__ __forceinline__ float4* part_rows(const KParams& p, int slot, int R, int DH) {
+    return reinterpret_cast<float4*>(p.part + (size_t)slot * R * DH);
+}
+__device__ __forceinline__ float2* part_sums(const KParams& p, int slot, int R, int DH) {
+    return reinterpret_cast<float2*>(p.part + (size_t)2 * p.many * R * DH) + (size_t)slot * R;
+}
 
-// SOLO: every warp has a share of its own (many heads: nothing is joined through shared memory and no warp
-// waits for another); otherwise a block's warps go through one share together (few heads, long contexts).
-template <typename T, int NG, int NT, int W, int NS, int MB, bool SOLO>
+template <typename T, int NG, int NT, int W, int NS, int MB>
 __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     using L = Blk<NG>;
-    constexpr int M = SOLO ? 1 : W;                               // warps of a share
-    constexpr int kSnap = SOLO ? 2 : W, kLeast = SOLO ? 1 : 2;
-    constexpr int R = 8 * NT, DH = 32 * NG;
+    constexpr int R = 8 * NT, DH = 32 * NG, kSnap = 2;
     constexpr uint32_t kTile = 2 * L::kBytes;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring = smem;                                         // [W][NS][kTile]
-    float* join = reinterpret_cast<float*>(smem + W * NS * kTile);
-    float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(join) + join_bytes<NG, W, SOLO>());   // [W][R], not SOLO
-    uint64_t* bars = reinterpret_cast<uint64_t*>(ml + (SOLO ? 0 : W * R));     // [W][NS]
-    int64_t* scan = reinterpret_cast<int64_t*>(bars + W * NS);    // [W]
-    int64_t* starts = scan + W;                                   // [threads]
-    int* s_last = reinterpret_cast<int*>(starts + 32 * W);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W * NS * kTile);   // [W][NS]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const Batch& bt = p.a.b;
 
-    // ---------------------------------------------------- this block's share of the line
-    if (threadIdx.x < W * NS) ub_init(&bars[threadIdx.x], 1);
+    // ------------------------------------------------------------------ the line and its cuts
+    if (lane < NS) ub_init(&bars[warp * NS + lane], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
     um::pdl_trigger();
     um::pdl_wait();
-    constexpr int kThreads = 32 * W;
-    const int per = (bt.B + kThreads - 1) / kThreads;
     auto units_of_head = [&](const Seq& q) -> int64_t {           // of each kv head of a sequence
         const int nrt = (q.n * p.G + R - 1) / R;
         int64_t sum = 0;
         for (int t = 0; t < nrt; ++t) sum += Place<R>::units_of(Place<R>::keys_of(t, q.n, q.len, q.ok, p.G));
         return sum;
     };
-    int64_t mine = 0;
-    for (int i = 0, sq = threadIdx.x * per; i < per && sq < bt.B; ++i, ++sq) mine += units_of_head(seq_of(bt, sq)) * p.kvh;
-    int64_t pref = mine;
+    // a lane a sequence, 32 at a time: the units before it and its own
+    auto sequences = [&](int s0, int64_t& mine, int64_t& before) {
+        mine = s0 + lane < bt.B ? units_of_head(seq_of(bt, s0 + lane)) * p.kvh : 0;
+        before = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, pref, o);
-        if (lane >= o) pref += v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
+        }
+        const int64_t sum = __shfl_sync(0xffffffffu, before, 31);
+        before -= mine;
+        return sum;
+    };
+    int64_t mine, before, total = sequences(0, mine, before);
+    for (int s0 = 32; s0 < bt.B; s0 += 32) {
+        int64_t m, b;
+        total += sequences(s0, m, b);
     }
-    if (lane == 31) scan[warp] = pref;
-    __syncthreads();
-    int64_t total = 0, below = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        if (w < warp) below += scan[w];
-        total += scan[w];
-    }
-    starts[threadIdx.x] = below + pref - mine;                    // units before this thread's sequences
-    __syncthreads();
-    // Equal shares, the first of them one unit longer where they do not divide; no more shares than units.
-    // A cut within kSnap units of a head's end moves to that end: joining a cut head costs more.
-    const int shares = (int)min((int64_t)(gridDim.x * (SOLO ? W : 1)), max((int64_t)1, total / kLeast));
-    const int id = SOLO ? blockIdx.x * W + warp : blockIdx.x;
+    if (total == 0) return;
+    // Equal shares, the first of them one unit longer where they do not divide; no more shares than units.  A cut
+    // within kSnap units of a head's end moves to that end: a cut head costs about as much.
+    const int shares = (int)min((int64_t)gridDim.x * W, total), id = blockIdx.x * W + warp;
+    if (id >= shares) return;
     const int64_t each = quotient(total, shares);
     const int longer = (int)(total - each * shares);
-    if (total == 0 || id >= shares) return;                       // all warps of a block that shares
     Place<R> at;                                                  // where the share stands
     int64_t lo, hi;
     {
-        // lane 0 finds the share's begin, the other lanes its end
+        // lane 0 keeps the share's begin, the other lanes its end
         const int k = id + (lane != 0);
         const int64_t raw = each * k + min(k, longer);
-        int64_t bound = total;
+        int64_t bound = total, in = 0;
         at.b = at.hk = at.rt = at.u = 0;
+        int64_t done = 0;
+        for (int s0 = 0; s0 < bt.B; s0 += 32) {
+            int64_t sum;
+            if (s0 == 0) sum = __shfl_sync(0xffffffffu, before + mine, 31);
+            else sum = sequences(s0, mine, before);
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                const int64_t x = __shfl_sync(0xffffffffu, raw, side) - done;
+                const uint32_t here = __ballot_sync(0xffffffffu, x >= before && x < before + mine);
+                if (here) {
+                    const int from = __ffs(here) - 1;
+                    const int64_t b0 = __shfl_sync(0xffffffffu, before, from);
+                    if ((lane != 0) == side) {
+                        at.b = s0 + from;
+                        in = x - b0;
+                    }
+                }
+            }
+            done += sum;
+        }
         if (raw < total) {
-            int a = 0, z = kThreads;                              // the last thread that starts at or before raw
-            while (z - a > 1) {
-                const int m = (a + z) >> 1;
-                if (starts[m] <= raw) a = m;
-                else z = m;
-            }
-            int64_t in = raw - starts[a], head;
-            at.b = a * per;
-            for (;; ++at.b) {
-                head = units_of_head(seq_of(bt, at.b));
-                if (in < head * p.kvh) break;
-                in -= head * p.kvh;
-            }
+            at.load_seq(p);
+            const int64_t head = units_of_head(Seq{at.row0, at.n, at.len, at.ok != 0});
             at.hk = (int)quotient(in, head);
             in -= head * at.hk;
-            at.load_seq(p);
             for (;; ++at.rt) {
                 at.load_tile(p);
                 if (in < at.units) break;
@@ -274,20 +275,21 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
         at.u = __shfl_sync(0xffffffffu, at.u, 0);
     }
     if (lo >= hi) return;
+    int st = 0;
+    uint32_t phase = 0;
+    uint8_t* my_ring = ring + warp * NS * kTile;
+    uint64_t* my_bar = bars + warp * NS;
+    bool failed = false;
     at.load_seq(p);
     at.load_tile(p);
     at.advance(p, 0);
 
     // ------------------------------------------------------------ the warp's ring of copies
-    uint8_t* my_ring = ring + warp * NS * kTile;
-    uint64_t* my_bar = bars + warp * NS;
     Place<R> ahead = at;                                          // the next unit to ask for
     const int share = (int)min(hi - lo, (int64_t)0x7fffffff);     // its units
-    int left = share - (SOLO ? 0 : warp);                         // of them, from `ahead` on
-    if (!SOLO && left > 0) ahead.advance(p, warp);
+    int left = share;                                             // of them, from `ahead` on
     int page0 = -1, page1 = -1;
-    uint32_t lacks = 0, phase = 0;                                // blocks that were not copied, 2 bits a stage
-    bool failed = false;
+    uint32_t lacks = 0;                                           // blocks that were not copied, 2 bits a stage
     auto look_up = [&]() {                                        // the pages of `ahead`, used one round later
         if (left <= 0) return;
         const int pos = ahead.u * kUnit;
@@ -324,9 +326,8 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                 }
             }
         }
-        left -= M;
-        ahead.u += M;
-        if (ahead.u >= ahead.units && left > 0) ahead.advance(p, 0);
+        --left;
+        if (++ahead.u >= ahead.units && left > 0) ahead.advance(p, 0);
         look_up();
     };
     look_up();
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     for (int i = 0; i < NS; ++i) ask(i);
 
     // -------------------------------------------------------------------- the share's heads
-    int st = 0, x = 0;
+    int x = 0;
     while (x < share) {
         const int u0 = at.u, u1 = min(at.units, u0 + (share - x));
         State<NG, NT> s;
@@ -417,9 +418,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
         }
         const int clear_to = at.len - at.n + at.rt * R / p.G + 1; // positions that every row sees
 
-        // the warp's units of this head
-        const int first = SOLO ? 0 : (warp - x) & (W - 1);
-        for (int u = u0 + first; u < u1 && !failed; u += M) {
+        for (int u = u0; u < u1 && !failed; ++u) {
             const uint8_t* tile = my_ring + st * kTile;
             const uint32_t have = 3u & ~(lacks >> (2 * st));
             if (!ub_try(&my_bar[st], phase)) {
@@ -637,7 +636,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
             }
         }
 
-        // ------------------------------------------------ the warps' states become one
+        // ------------------------------------------- the head's rows, or this share's part of them
         // the sums over r of l; codes' and zeros' parts together, in true units
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -655,72 +654,25 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                     }
                 }
             }
-        auto join_warps = [&]() {                                 // warp 0 ends up with the sum
-            if constexpr (!SOLO) {
-            if (r == 0) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) ml[warp * R + t * 8 + 2 * c + i] = make_float2(s.off[t][i], s.l[t][i]);
-            }
-            __syncthreads();
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float m = -INFINITY, l = 0.f;
-                    for (int w = 0; w < W; ++w) m = fmaxf(m, ml[w * R + t * 8 + 2 * c + i].x);
-                    const float base = m == -INFINITY ? 0.f : m;
-                    for (int w = 0; w < W; ++w) {
-                        const float2 v = ml[w * R + t * 8 + 2 * c + i];
-                        l += v.y * ex2(v.x - base);
-                    }
-                    const float f = ex2(s.off[t][i] - base);
-                    s.off[t][i] = m;
-                    s.l[t][i] = l;
-#pragma unroll
-                    for (int d = 0; d < 2 * NG; ++d) {
-                        s.o[d][t][i] *= f;
-                        s.o[d][t][i + 2] *= f;
-                    }
-                }
-            // half of the warps hand over at a time, 8 rows at a time
-#pragma unroll
-            for (int h = W / 2; h >= 1; h >>= 1)
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float* at_join = join + (size_t)(warp & (h - 1)) * (8 * NG * 32) + lane;
-                    if (warp >= h && warp < 2 * h) {
-#pragma unroll
-                        for (int d = 0; d < 2 * NG; ++d)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) at_join[(4 * d + i) * 32] = s.o[d][t][i];
-                    }
-                    __syncthreads();
-                    if (warp < h) {
-#pragma unroll
-                        for (int d = 0; d < 2 * NG; ++d)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) s.o[d][t][i] += at_join[(4 * d + i) * 32];
-                    }
-                    if (h > 1 || t + 1 < NT) __syncthreads();
-                }
-            }
-        };
-        const bool speaks = SOLO || warp == 0;                    // has the share's state
-        bool row_in[NT][2];
+        const bool whole = u0 == 0 && u1 == at.units;
+        uint2 cuts = make_uint2(0u, 0u);                          // from this share on, how many more
+        if (u0 == 0 && !whole) {
+            // the shares whose cuts fall inside the head, as the plan above cuts
+            const int64_t unit = lo + x + at.units - kSnap, bend = (each + 1) * longer;
+            const int past = unit <= bend ? (int)quotient(unit + each, each + 1) : longer + (int)quotient(unit - bend + each - 1, each);
+            cuts = make_uint2((uint32_t)id, (uint32_t)(past - 1 - id));
+        }
+        const int slot = 2 * id + (u0 == 0);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) row_in[t][i] = at.rt * R + t * 8 + 2 * c + i < rows;
-        auto write_out = [&]() {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int row = at.rt * R + t * 8 + 2 * c + i;
-                    if (!row_in[t][i]) continue;
-                    T* to = static_cast<T*>(p.a.out) + (int64_t)(at.row0 + row / p.G) * p.a.ldo + (int64_t)(at.hk * p.G + row % p.G) * DH + 4 * r;
+            for (int i = 0; i < 2; ++i) {
+                const int in = t * 8 + 2 * c + i, row = at.rt * R + in;
+                if (row >= rows) continue;
+                const int token = at.row0 + row / p.G, head = at.hk * p.G + row % p.G;
+                if (u0 == 0 && r == 0) p.meta[(int64_t)token * p.nh + head] = make_uint2(cuts.x | ((uint32_t)in << 24), cuts.y);
+                if (whole) {
+                    T* to = static_cast<T*>(p.a.out) + (int64_t)token * p.a.ldo + (int64_t)head * DH + 4 * r;
                     const float inv = s.l[t][i] == 0.f ? 0.f : 1.f / s.l[t][i];
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
@@ -732,85 +684,14 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                             for (int k = 0; k < 4; ++k) to[32 * g + k] = v[k];
                         }
                     }
+                } else {
+                    float4* to = part_rows(p, slot, R, DH) + in * (DH / 4) + r;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        __stcg(to + 8 * g, make_float4(s.o[2 * g][t][i], s.o[2 * g][t][i + 2], s.o[2 * g + 1][t][i], s.o[2 * g + 1][t][i + 2]));
+                    if (r == 0) __stcg(part_sums(p, slot, R, DH) + in, make_float2(s.off[t][i], s.l[t][i]));
                 }
-        };
-        join_warps();
-        if (u0 == 0 && u1 == at.units) {
-            if (speaks) write_out();
-        } else {
-            // the head's stretch of the line and the shares whose cuts fall inside it, as the plan above cuts
-            constexpr int kSlot = NT * 8 * NG * 32 + 2 * R;
-            const int64_t head_lo = lo + x - u0;
-            auto share_from = [&](int64_t unit) -> int {          // the first share that begins there or later
-                const int64_t bend = (each + 1) * longer;
-                return unit <= bend ? (int)quotient(unit + each, each + 1) : longer + (int)quotient(unit - bend + each - 1, each);
-            };
-            const int c_first = share_from(head_lo + kSnap + 1) - 1, c_last = share_from(head_lo + at.units - kSnap) - 1;
-            bool last = false;
-            if (speaks) {
-                float* to = p.part + (size_t)(2 * id + (u0 == 0)) * kSlot;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (!row_in[t][i]) continue;
-#pragma unroll
-                        for (int d = 0; d < 2 * NG; ++d) {
-                            __stcg(to + ((d * NT + t) * 4 + i) * 32 + lane, s.o[d][t][i]);
-                            __stcg(to + ((d * NT + t) * 4 + i + 2) * 32 + lane, s.o[d][t][i + 2]);
-                        }
-                        if (r == 0)
-                            __stcg(reinterpret_cast<float2*>(to + NT * 8 * NG * 32) + t * 8 + 2 * c + i, make_float2(s.off[t][i], s.l[t][i]));
-                    }
-                __syncwarp();
-                if (lane == 0) {
-                    last = um::atom_acq_rel_add_u32(&p.tickets[c_first], 1u) == (uint32_t)(c_last - c_first);
-                    if (last) p.tickets[c_first] = 0;             // for the next call
-                }
-                last = __shfl_sync(0xffffffffu, last, 0);
-                if (!SOLO && lane == 0) *s_last = last;
             }
-            if constexpr (!SOLO) {
-                __syncthreads();
-                last = *s_last;
-            }
-            if (last) {
-                s.clear();
-                for (int o = c_first + (SOLO ? 0 : warp); o <= c_last; o += M) {
-                    const float* from = p.part + (size_t)(2 * o + (o == c_first)) * kSlot;
-                    float v[2 * NG][NT][4];
-                    float2 w[NT][2];
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const bool in = row_in[t][i];
-                            w[t][i] = in ? __ldcg(reinterpret_cast<const float2*>(from + NT * 8 * NG * 32) + t * 8 + 2 * c + i) : make_float2(-INFINITY, 0.f);
-#pragma unroll
-                            for (int d = 0; d < 2 * NG; ++d) {
-                                v[d][t][i] = in ? __ldcg(from + ((d * NT + t) * 4 + i) * 32 + lane) : 0.f;
-                                v[d][t][i + 2] = in ? __ldcg(from + ((d * NT + t) * 4 + i + 2) * 32 + lane) : 0.f;
-                            }
-                        }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float m = fmaxf(s.off[t][i], w[t][i].x), base = m == -INFINITY ? 0.f : m;
-                            const float f = ex2(s.off[t][i] - base), g = ex2(w[t][i].x - base);
-                            s.off[t][i] = m;
-                            s.l[t][i] = s.l[t][i] * f + w[t][i].y * g;
-#pragma unroll
-                            for (int d = 0; d < 2 * NG; ++d) {
-                                s.o[d][t][i] = s.o[d][t][i] * f + v[d][t][i] * g;
-                                s.o[d][t][i + 2] = s.o[d][t][i + 2] * f + v[d][t][i + 2] * g;
-                            }
-                        }
-                }
-                join_warps();
-                if (speaks) write_out();
-            }
-        }
         x += u1 - u0;
         if (x < share) {
             at.u = u1 - 1;
@@ -827,34 +708,135 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     }
 }
 
-// The shapes of a launch: warps and blocks at once as registers and the rings allow.
-template <int NG, int NT, bool SOLO> struct Shape {
-    static constexpr int W = SOLO ? 4 : NT == 1 ? (NG == 8 ? 8 : 16) : NT == 2 && NG < 8 ? 8 : 8;
-    static constexpr int NS = NG == 2 ? 4 : 2;
-    static constexpr int MB = SOLO ? (NG == 2 ? 4 : NG == 4 ? 3 : 2) : 1;
-    static constexpr size_t smem = (size_t)W * NS * 1280 * NG + join_bytes<NG, W, SOLO>() + (SOLO ? 0 : W * 8 * NT * 8) + W * NS * 8 +
-                                   W * 8 + 32 * W * 8 + 16;
-    static_assert(smem <= 227 * 1024 / MB - 1024, "");
-    static constexpr int shares = MB * (SOLO ? W : 1);           // of an SM
-    static constexpr size_t part_floats = (size_t)2 * shares * (NT * 8 * NG * 32 + 16 * NT);
-};
-constexpr int kMaxShares = 16;                                    // of an SM
-int most_rows(int ng) { return ng == 8 ? 2 : 4; }                 // 8-row tiles that a warp's registers hold
-template <int NG> constexpr size_t part_floats() {
-    return std::max(std::max(Shape<NG, 1, true>::part_floats, Shape<NG, 1, false>::part_floats),
-                    std::max(Shape<NG, 2, false>::part_floats, NG == 8 ? (size_t)0 : Shape<NG, 4, false>::part_floats));
+// The rows of cut heads: sums of the shares' parts in their order.  WPR warps a row: 1 where a head is cut into
+// a few shares, 16 where a few heads fill the device (their loads then go out together: the time is their latency).
+template <typename T, int NG, int R, int WPR>
+__global__ void __launch_bounds__(WPR == 1 ? 256 : 32 * WPR) k_join(const KParams p) {
+    constexpr int DH = 32 * NG, V = (NG + 3) / 4, LR = DH / 4 < 32 ? DH / 4 : 32;   // a row is LR lanes of V float4
+    __shared__ float4 acc_s[WPR][V][32];
+    __shared__ float2 ml_s[WPR];
+    // no early start for what comes next: blocks of the next call that wait on an SM slowed these (141 -> 127 us at
+    // 32 sequences of 1400 positions, 72 heads)
+    um::pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * 8 + warp : blockIdx.x;
+    if (row >= (int64_t)p.a.b.T * p.nh) return;
+    const int token = (int)(row / p.nh), head = (int)(row % p.nh);
+    const int sq = seq_of_row(p.a.b, token);
+    if (sq < 0) return;
+    if (p.a.b.start) {                                            // a row that the plan skipped has no entry
+        const Seq q = seq_of(p.a.b, sq);
+        if (q.n == 0) return;
+    }
+    const uint2 m = p.meta[row];
+    const int first = (int)(m.x & 0xffffffu), in = (int)(m.x >> 24), n = (int)m.y + 1;
+    if (n < 2) return;
+    float top = -INFINITY, l = 0.f;
+    float4 acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // 32 parts at a time: their exponents and sums a lane each, then their values
+    const int k1 = WPR == 1 ? n : n * (warp + 1) / WPR;           // the warp's stretch of the parts
+    for (int k0 = WPR == 1 ? 0 : n * warp / WPR; k0 < k1; k0 += 32) {
+        const int k = k0 + lane;
+        const float2 ml = k < k1 ? __ldcg(part_sums(p, 2 * (first + k) + (k == 0), R, DH) + in) : make_float2(-INFINITY, 0.f);
+        float mx = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = fmaxf(mx, top);
+        const float base = mx == -INFINITY ? 0.f : mx, f = ex2(top - base), w = ex2(ml.x - base);
+        top = mx;
+        l = l * f + warp_sum(ml.y * w);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = make_float4(acc[v].x * f, acc[v].y * f, acc[v].z * f, acc[v].w * f);
+        const int here = min(32, k1 - k0);
+        // a warp reads 32 / LR parts at once; the lanes past them repeat the last with no weight
+        constexpr int P = 32 / LR;
+#pragma unroll (WPR == 1 ? 4 : 16 / P)
+        for (int j = 0; j < here; j += P) {
+            const int mine = j + (P == 1 ? 0 : lane / LR);
+            const int at = min(mine, here - 1);
+            const float wj = __shfl_sync(0xffffffffu, w, at) * (mine < here ? 1.f : 0.f);
+            const float4* from = part_rows(p, 2 * (first + k0 + at) + (k0 + at == 0), R, DH) + in * (DH / 4) + lane % LR;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float4 x = __ldcg(from + 32 * v);
+                if (mine < here) {
+                    acc[v].x = fmaf(x.x, wj, acc[v].x);
+                    acc[v].y = fmaf(x.y, wj, acc[v].y);
+                    acc[v].z = fmaf(x.z, wj, acc[v].z);
+                    acc[v].w = fmaf(x.w, wj, acc[v].w);
+                }
+            }
+        }
+    }
+    if constexpr (WPR > 1) {
+        if (lane == 0) ml_s[warp] = make_float2(top, l);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc_s[warp][v][lane] = acc[v];
+        __syncthreads();
+        if (warp > 0) return;
+        float mx = -INFINITY;
+        for (int w = 0; w < WPR; ++w) mx = fmaxf(mx, ml_s[w].x);
+        const float base = mx == -INFINITY ? 0.f : mx;
+        l = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) {
+            const float f = ex2(ml_s[w].x - base);
+            l += ml_s[w].y * f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float4 x = acc_s[w][v][lane];
+                acc[v].x = fmaf(x.x, f, acc[v].x);
+                acc[v].y = fmaf(x.y, f, acc[v].y);
+                acc[v].z = fmaf(x.z, f, acc[v].z);
+                acc[v].w = fmaf(x.w, f, acc[v].w);
+            }
+        }
+    }
+    if constexpr (LR < 32) {
+        acc[0].x += __shfl_xor_sync(0xffffffffu, acc[0].x, 16);
+        acc[0].y += __shfl_xor_sync(0xffffffffu, acc[0].y, 16);
+        acc[0].z += __shfl_xor_sync(0xffffffffu, acc[0].z, 16);
+        acc[0].w += __shfl_xor_sync(0xffffffffu, acc[0].w, 16);
+        if (lane >= LR) return;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* to = static_cast<T*>(p.a.out) + (int64_t)token * p.a.ldo + (int64_t)head * DH + 4 * lane;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        T o[4] = {DT<T>::r(acc[v].x * inv), DT<T>::r(acc[v].y * inv), DT<T>::r(acc[v].z * inv), DT<T>::r(acc[v].w * inv)};
+        if (p.ovec) *reinterpret_cast<uint2*>(to + 128 * v) = *reinterpret_cast<const uint2*>(o);
+        else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) to[128 * v + k] = o[k];
+        }
+    }
 }
 
-template <typename T, int NG, int NT, bool SOLO>
-cudaError_t go(const spffn_kv4_ctx& c, const KParams& p, cudaStream_t st) {
-    using S = Shape<NG, NT, SOLO>;
-    auto kern = k_attend<T, NG, NT, S::W, S::NS, S::MB, SOLO>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
-    if (e != cudaSuccess) return e;
+// The shapes of a launch: warps and blocks at once as registers and the rings allow.
+template <int NG, int NT> struct Shape {
+    static constexpr int W = 4;
+    static constexpr int NS = NG == 2 ? 4 : NG == 4 ? 3 : 2;
+    static constexpr int MB = NG == 2 ? (NT == 1 ? 4 : 2) : NG == 4 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 2 : 2);
+    static constexpr size_t smem = (size_t)W * NS * 1280 * NG + W * NS * 8;
+    static_assert(smem <= 227 * 1024 / MB - 1024, "");
+    static constexpr int shares = MB * W;                         // of an SM
+    static constexpr size_t part_floats = (size_t)2 * shares * 8 * NT * (32 * NG + 2);
+};
+constexpr int most_rows(int ng) { return ng == 2 ? 4 : 2; }       // 8-row tiles that a warp's registers hold
+template <int NG> constexpr size_t part_floats() {
+    return std::max(std::max(Shape<NG, 1>::part_floats, Shape<NG, 2>::part_floats), NG == 2 ? Shape<NG, 4>::part_floats : (size_t)0);
+}
+
+template <typename K>
+cudaError_t launch_chained(K kern, unsigned grid, unsigned threads, size_t smem, const KParams& p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(c.sms * S::MB));
-    cfg.blockDim = dim3(32 * S::W);
-    cfg.dynamicSmemBytes = S::smem;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -864,21 +846,36 @@ cudaError_t go(const spffn_kv4_ctx& c, const KParams& p, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+template <typename T, int NG, int NT>
+cudaError_t go(const spffn_kv4_ctx& c, KParams p, cudaStream_t st) {
+    using S = Shape<NG, NT>;
+    auto kern = k_attend<T, NG, NT, S::W, S::NS, S::MB>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
+    if (e != cudaSuccess) return e;
+    p.many = c.sms * S::shares;
+    e = launch_chained(kern, (unsigned)(c.sms * S::MB), 32 * S::W, S::smem, p, st);
+    if (e != cudaSuccess) return e;
+    // a row tile is cut into about as many parts as there are warps for it
+    const int64_t rows = (int64_t)p.a.b.T * p.nh, tiles = std::max<int64_t>(p.a.b.B, (int64_t)p.a.b.T * p.G / (8 * NT)) * p.kvh;
+    if (tiles * 16 <= (int64_t)c.sms * S::MB * S::W)
+        return launch_chained(k_join<T, NG, 8 * NT, 16>, (unsigned)rows, 512, 0, p, st);
+    return launch_chained(k_join<T, NG, 8 * NT, 1>, (unsigned)((rows + 7) / 8), 256, 0, p, st);
+}
+
 template <typename T, int NG>
-cudaError_t by_rows(const spffn_kv4_ctx& c, const KParams& p, int nt, bool solo, cudaStream_t st) {
-    if (nt == 1) return solo ? go<T, NG, 1, true>(c, p, st) : go<T, NG, 1, false>(c, p, st);
-    if constexpr (NG < 8) {
-        if (nt == 4) return go<T, NG, 4, false>(c, p, st);
+cudaError_t by_rows(const spffn_kv4_ctx& c, const KParams& p, int nt, cudaStream_t st) {
+    if constexpr (most_rows(NG) == 4) {
+        if (nt == 4) return go<T, NG, 4>(c, p, st);
     }
-    return go<T, NG, 2, false>(c, p, st);
+    return nt == 1 ? go<T, NG, 1>(c, p, st) : go<T, NG, 2>(c, p, st);
 }
 
 template <typename T>
-cudaError_t by_width(const spffn_kv4_ctx& c, const KParams& p, int nt, bool solo, cudaStream_t st) {
+cudaError_t by_width(const spffn_kv4_ctx& c, const KParams& p, int nt, cudaStream_t st) {
     switch (c.cfg.dh) {
-        case 64: return by_rows<T, 2>(c, p, nt, solo, st);
-        case 128: return by_rows<T, 4>(c, p, nt, solo, st);
-        default: return by_rows<T, 8>(c, p, nt, solo, st);
+        case 64: return by_rows<T, 2>(c, p, nt, st);
+        case 128: return by_rows<T, 4>(c, p, nt, st);
+        default: return by_rows<T, 8>(c, p, nt, st);
     }
 }
 
@@ -888,8 +885,8 @@ Layout layout(const spffn_kv4_config& c, int sms) {
     Layout l;
     const size_t part = c.dh == 64 ? part_floats<2>() : c.dh == 128 ? part_floats<4>() : part_floats<8>();
     l.ctl = 0;
-    l.tickets = kCtlBytes;
-    l.part = align_up(l.tickets + (size_t)sms * kMaxShares * sizeof(uint32_t), 256);
+    l.meta = kCtlBytes;
+    l.part = align_up(l.meta + (size_t)c.max_tokens * c.nh * sizeof(uint2), 256);
     l.total = l.part + sms * part * sizeof(float);
     return l;
 }
@@ -899,19 +896,19 @@ cudaError_t launch_attend(const spffn_kv4_ctx& c, const AttendArgs& a, cudaStrea
     p.a = a;
     p.pool = c.pool;
     p.part = reinterpret_cast<float*>(c.ws + c.lay.part);
-    p.tickets = reinterpret_cast<uint32_t*>(c.ws + c.lay.tickets);
+    p.meta = reinterpret_cast<uint2*>(c.ws + c.lay.meta);
+    p.many = 0;
     p.nh = c.cfg.nh;
     p.kvh = c.cfg.kvh;
     p.G = c.cfg.nh / c.cfg.kvh;
     p.qvec = aligned_to(a.q, 16) && a.ldq % 8 == 0;
+    p.ovec = aligned_to(a.out, 8) && a.ldo % 4 == 0;
     p.head_bytes = (uint32_t)(c.cfg.page_size / 16) * (20u * c.cfg.dh);
     p.page_bytes = p.head_bytes * (uint32_t)c.cfg.kvh;
-    p.ovec = aligned_to(a.out, 8) && a.ldo % 4 == 0;
     // 8, 16 or 32 query rows a tile, by the rows that a kv head has in the mean
     const int64_t rows = ((int64_t)a.b.T + a.b.B - 1) / a.b.B * p.G;
     const int nt = std::min(rows <= 8 ? 1 : rows <= 16 ? 2 : 4, most_rows(c.cfg.dh / 32));
-    const bool solo = (int64_t)a.b.B * c.cfg.kvh >= SOLO_MIN;
-    return c.cfg.dtype == SPFFN_BF16 ? by_width<__nv_bfloat16>(c, p, nt, solo, st) : by_width<__half>(c, p, nt, solo, st);
+    return c.cfg.dtype == SPFFN_BF16 ? by_width<__nv_bfloat16>(c, p, nt, st) : by_width<__half>(c, p, nt, st);
 }
 
 }  // namespace kv4
