@@ -291,31 +291,31 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     int page0 = -1, page1 = -1;
     uint32_t lacks = 0;                                           // blocks that were not copied, 2 bits a stage
     auto look_up = [&]() {                                        // the pages of `ahead`, used one round later
-        if (left <= 0) return;
         const int pos = ahead.u * kUnit;
         const int32_t* row = bt.table + ahead.b * bt.ldt + (pos >> bt.page_log);
-        page0 = pos < ahead.keys ? __ldg(row) : -1;
+        page0 = pos < ahead.keys ? __ldg(row) : -1;               // no positions: a refused sequence
         if (bt.page_log == 4) page1 = pos + 16 < ahead.keys ? __ldg(row + 1) : -1;
     };
+    const bool small = bt.page_log == 4;                          // a unit is two pages
     auto source = [&](int page, int pp) {
         return p.pool + (uint64_t)(uint32_t)page * p.page_bytes +
                ((uint32_t)ahead.hk * p.head_bytes + (uint32_t)((pp & (bt.page - 1)) >> 4) * L::kBytes);
     };
     auto ask = [&](int st) {
-        if (left <= 0 || failed) return;
+        if (left <= 0) return;
         const int pos = ahead.u * kUnit;
         uint64_t* bar = &my_bar[st];
         const uint32_t dst = s32(my_ring + st * kTile);
-        if (lacks) lacks &= ~(3u << (2 * st));
-        if (bt.page_log > 4 && (unsigned)page0 < (unsigned)bt.pages) {
+        lacks &= ~(3u << (2 * st));
+        if (!small && (unsigned)page0 < (unsigned)bt.pages) {
             // one stretch; where the row's positions end in its first block the second comes along unread
             if (lane == 0) {
                 ub_expect(bar, kTile);
                 bulk_copy(dst, source(page0, pos), kTile, bar);
             }
         } else {
-            const bool in0 = (unsigned)page0 < (unsigned)bt.pages, in1 = bt.page_log == 4 && (unsigned)page1 < (unsigned)bt.pages;
-            if (((pos < ahead.keys && !in0) || (bt.page_log == 4 && pos + 16 < ahead.keys && !in1)) && lane == 0) latch(bt.err, ERR_PAGE_RANGE);
+            const bool in0 = (unsigned)page0 < (unsigned)bt.pages, in1 = small && (unsigned)page1 < (unsigned)bt.pages;
+            if (((pos < ahead.keys && !in0) || (small && pos + 16 < ahead.keys && !in1)) && lane == 0) latch(bt.err, ERR_PAGE_RANGE);
             lacks |= ((in0 ? 0u : 1u) | (in1 ? 0u : 2u)) << (2 * st);
             if (lane == 0) {
                 if (!in0 && !in1) um::ub_arrive(bar);
@@ -326,8 +326,8 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                 }
             }
         }
-        --left;
-        if (++ahead.u >= ahead.units && left > 0) ahead.advance(p, 0);
+        if (--left <= 0) return;
+        if (++ahead.u >= ahead.units) ahead.advance(p, 0);
         look_up();
     };
     look_up();
@@ -447,7 +447,6 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                     top = __float2half2_rn(0.f);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        if (!((have >> j) & 1u)) continue;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             uint32_t v[NG];
@@ -463,24 +462,24 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
 #pragma unroll
                     for (int o = 1; o < 4; o <<= 1) top = __hmax2_nan(top, as_h2(__shfl_xor_sync(0xffffffffu, as_u(top), o)));
                 };
-                const bool edge = p0 + kUnit > at.keys;
+                const bool edge = p0 + kUnit > at.keys || have != 3u;
                 if (!edge) tops();
                 if (edge || __hisnan(__low2half(top)) || __hisnan(__high2half(top))) {
                     uint8_t* w = const_cast<uint8_t*>(tile);
-                    const int j = lane >> 4, tok = lane & 15;     // a lane a position
-                    if ((have >> j) & 1u) {
-                        bool nan = false;
+                    uint8_t* blk = w + (lane >> 4) * L::kBytes;   // a lane a position
+                    const int tok = lane & 15;
+                    const bool here = (have >> (lane >> 4)) & 1u;
+                    bool nan = false;
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) nan |= __hisnan(*reinterpret_cast<const __half*>(w + j * L::kBytes + L::vs(tok, g)));
-                        if (nan || p0 + lane >= at.keys) {
+                    for (int g = 0; g < NG; ++g) nan |= __hisnan(*reinterpret_cast<const __half*>(blk + L::vs(tok, g)));
+                    if (nan || !here || p0 + lane >= at.keys) {
 #pragma unroll
-                            for (int g = 0; g < NG; ++g) {
-                                *reinterpret_cast<uint16_t*>(w + j * L::kBytes + L::vs(tok, g)) = 0;
-                                *reinterpret_cast<uint16_t*>(w + j * L::kBytes + L::vz(tok, g)) = 0;
-                            }
-                            nan_tok = nan ? 1u << lane : 0u;
+                        for (int g = 0; g < NG; ++g) {
+                            *reinterpret_cast<uint16_t*>(blk + L::vs(tok, g)) = 0;
+                            *reinterpret_cast<uint16_t*>(blk + L::vz(tok, g)) = 0;
                         }
                     }
+                    nan_tok = nan && here ? 1u << lane : 0u;
                     um::fence_async_smem();                       // the ring's next copy comes by another proxy
                     nan_tok = __reduce_or_sync(0xffffffffu, nan_tok);
                     __syncwarp();
@@ -500,11 +499,10 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                     lds<NG>(w1, blk + (r + 8) * 16 * NG + c * 4 * NG);
                     lds<NG / 2>(st0, blk + L::kKs + r * 2 * NG);
                     lds<NG / 2>(st1, blk + L::kKs + (r + 8) * 2 * NG);
-                    uint32_t z0 = 0, z1 = 0;
-                    if (2 * c < NG) {
-                        z0 = *reinterpret_cast<const uint32_t*>(blk + L::kKz + r * 2 * NG + 4 * c);
-                        z1 = *reinterpret_cast<const uint32_t*>(blk + L::kKz + (r + 8) * 2 * NG + 4 * c);
-                    }
+                    const int zc = NG == 8 ? 4 * c : 4 * (c & (NG / 2 - 1));          // groups 2c, 2c + 1
+                    uint32_t z0 = *reinterpret_cast<const uint32_t*>(blk + L::kKz + r * 2 * NG + zc);
+                    uint32_t z1 = *reinterpret_cast<const uint32_t*>(blk + L::kKz + (r + 8) * 2 * NG + zc);
+                    if (NG < 8 && 2 * c >= NG) z0 = z1 = 0u;
                     float part[NT][4];
 #pragma unroll
                     for (int t = 0; t < NT; ++t) mma0(sc[j][t], z0, z1, z0, z1, qs[t][0], qs[t][1]);
@@ -593,18 +591,15 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                     }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    if (!((have >> j) & 1u)) continue;
                     const uint8_t* blk = tile + j * L::kBytes;
                     uint32_t w0[NG], w1[NG], s0[NG], s1[NG];       // words of tokens 2c, 2c + 1 | 2c + 8, 2c + 9
                     lds<NG>(w0, blk + L::kV + r * 16 * NG + c * 4 * NG);
                     lds<NG>(w1, blk + L::kV + 128 * NG + r * 16 * NG + c * 4 * NG);
                     lds<NG>(s0, blk + L::kVs + c * 4 * NG);
                     lds<NG>(s1, blk + L::kVs + 16 * NG + c * 4 * NG);
-                    uint32_t z0 = 0, z1 = 0;
-                    if (r < NG) {
-                        z0 = *reinterpret_cast<const uint32_t*>(blk + L::kVz + c * 4 * NG + 4 * r);
-                        z1 = *reinterpret_cast<const uint32_t*>(blk + L::kVz + 16 * NG + c * 4 * NG + 4 * r);
-                    }
+                    uint32_t z0 = *reinterpret_cast<const uint32_t*>(blk + L::kVz + c * 4 * NG + 4 * (r & (NG - 1)));
+                    uint32_t z1 = *reinterpret_cast<const uint32_t*>(blk + L::kVz + 16 * NG + c * 4 * NG + 4 * (r & (NG - 1)));
+                    if (r >= NG) z0 = z1 = 0u;
 #pragma unroll
                     for (int t = 0; t < NT; ++t) mma(oz[t], z0, 0u, z1, 0u, pb[j][t][0], pb[j][t][1]);
 #pragma unroll
