@@ -40,6 +40,7 @@ using um::ub_init;
 using um::ub_try;
 
 constexpr int kUnit = 32;             // positions of a unit
+constexpr int kHead = 1;              // what a head costs beside its units, in units: its q, its sums, its rows
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct KParams {
@@ -141,14 +142,6 @@ template <int R> struct Place {
         }
         load_tile(p);
     }
-    __device__ __forceinline__ void advance(const KParams& p, int by) {
-        u += by;
-        while (u >= units) {
-            u -= units;
-            next_pair(p);
-            if (b >= p.a.b.B) return;
-        }
-    }
 };
 
 // The running state of a tile of 8 NT query rows: thread (r, c) = (lane / 4, lane % 4) holds query columns
@@ -193,10 +186,10 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     __syncwarp();
     um::pdl_trigger();
     um::pdl_wait();
-    auto units_of_head = [&](const Seq& q) -> int64_t {           // of each kv head of a sequence
+    auto units_of_head = [&](const Seq& q) -> int64_t {           // length in the line of each kv head of a sequence
         const int nrt = (q.n * p.G + R - 1) / R;
         int64_t sum = 0;
-        for (int t = 0; t < nrt; ++t) sum += Place<R>::units_of(Place<R>::keys_of(t, q.n, q.len, q.ok, p.G));
+        for (int t = 0; t < nrt; ++t) sum += kHead + Place<R>::units_of(Place<R>::keys_of(t, q.n, q.len, q.ok, p.G));
         return sum;
     };
     // a lane a sequence, 32 at a time: the units before it and its own
@@ -225,12 +218,13 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     const int64_t each = quotient(total, shares);
     const int longer = (int)(total - each * shares);
     Place<R> at;                                                  // where the share stands
-    int64_t lo, hi;
+    int64_t line, line_end;                                       // where its row tile begins in the line; the same of
+    int u_end;                                                    // the share's end, and the unit there
     {
         // lane 0 keeps the share's begin, the other lanes its end
         const int k = id + (lane != 0);
         const int64_t raw = each * k + min(k, longer);
-        int64_t bound = total, in = 0;
+        int64_t bound = total, in = 0;                            // the row tile's begin
         at.b = at.hk = at.rt = at.u = 0;
         int64_t done = 0;
         for (int s0 = 0; s0 < bt.B; s0 += 32) {
@@ -259,22 +253,29 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
             in -= head * at.hk;
             for (;; ++at.rt) {
                 at.load_tile(p);
-                if (in < at.units) break;
-                in -= at.units;
+                if (in < kHead + at.units) break;
+                in -= kHead + at.units;
             }
-            at.u = (int)in;
+            bound = raw - in;
+            at.u = max(0, (int)in - kHead);
             if (at.u <= kSnap) at.u = 0;
-            else if (at.units - at.u <= kSnap) at.u = at.units;
-            bound = raw + (at.u - in);
+            else if (at.units - at.u <= kSnap) {                  // the next one's begin
+                at.u = 0;
+                bound += kHead + at.units;
+                at.next_pair(p);
+            }
         }
-        lo = __shfl_sync(0xffffffffu, bound, 0);
-        hi = __shfl_sync(0xffffffffu, bound, 1);
+        line = __shfl_sync(0xffffffffu, bound, 0);
+        line_end = __shfl_sync(0xffffffffu, bound, 1);
+        u_end = __shfl_sync(0xffffffffu, at.u, 1);
         at.b = __shfl_sync(0xffffffffu, at.b, 0);
         at.hk = __shfl_sync(0xffffffffu, at.hk, 0);
         at.rt = __shfl_sync(0xffffffffu, at.rt, 0);
         at.u = __shfl_sync(0xffffffffu, at.u, 0);
     }
-    if (lo >= hi) return;
+    if (line > line_end || (line == line_end && at.u >= u_end)) return;
+    at.load_seq(p);
+    at.load_tile(p);
     int st = 0;
     uint32_t phase = 0;
     uint8_t* my_ring = ring + warp * NS * kTile;
@@ -282,12 +283,11 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     bool failed = false;
     at.load_seq(p);
     at.load_tile(p);
-    at.advance(p, 0);
 
     // ------------------------------------------------------------ the warp's ring of copies
     Place<R> ahead = at;                                          // the next unit to ask for
-    const int share = (int)min(hi - lo, (int64_t)0x7fffffff);     // its units
-    int left = share;                                             // of them, from `ahead` on
+    int64_t line_ahead = line;
+    int stop = line_ahead == line_end ? u_end : ahead.units;      // of its row tile; 0 once the share is through
     int page0 = -1, page1 = -1;
     uint32_t lacks = 0;                                           // blocks that were not copied, 2 bits a stage
     auto look_up = [&]() {                                        // the pages of `ahead`, used one round later
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                ((uint32_t)ahead.hk * p.head_bytes + (uint32_t)((pp & (bt.page - 1)) >> 4) * L::kBytes);
     };
     auto ask = [&](int st) {
-        if (left <= 0) return;
+        if (stop == 0) return;
         const int pos = ahead.u * kUnit;
         uint64_t* bar = &my_bar[st];
         const uint32_t dst = s32(my_ring + st * kTile);
@@ -326,8 +326,14 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                 }
             }
         }
-        if (--left <= 0) return;
-        if (++ahead.u >= ahead.units) ahead.advance(p, 0);
+        if (++ahead.u == stop) {
+            line_ahead += kHead + ahead.units;
+            stop = 0;
+            if (line_ahead > line_end || (line_ahead == line_end && u_end == 0)) return;
+            ahead.u = 0;
+            ahead.next_pair(p);
+            stop = line_ahead == line_end ? u_end : ahead.units;
+        }
         look_up();
     };
     look_up();
@@ -335,9 +341,8 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     for (int i = 0; i < NS; ++i) ask(i);
 
     // -------------------------------------------------------------------- the share's heads
-    int x = 0;
-    while (x < share) {
-        const int u0 = at.u, u1 = min(at.units, u0 + (share - x));
+    for (;;) {
+        const int u0 = at.u, u1 = line == line_end ? u_end : at.units;
         State<NG, NT> s;
         s.clear();
         float oz[NT][4];
@@ -653,7 +658,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
         uint2 cuts = make_uint2(0u, 0u);                          // from this share on, how many more
         if (u0 == 0 && !whole) {
             // the shares whose cuts fall inside the head, as the plan above cuts
-            const int64_t unit = lo + x + at.units - kSnap, bend = (each + 1) * longer;
+            const int64_t unit = line + kHead + at.units - kSnap, bend = (each + 1) * longer;
             const int past = unit <= bend ? (int)quotient(unit + each, each + 1) : longer + (int)quotient(unit - bend + each - 1, each);
             cuts = make_uint2((uint32_t)id, (uint32_t)(past - 1 - id));
         }
@@ -687,11 +692,10 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                     if (r == 0) __stcg(part_sums(p, slot, R, DH) + in, make_float2(s.off[t][i], s.l[t][i]));
                 }
             }
-        x += u1 - u0;
-        if (x < share) {
-            at.u = u1 - 1;
-            at.advance(p, 1);
-        }
+        line += kHead + at.units;
+        if (failed || line > line_end || (line == line_end && u_end == 0)) break;
+        at.u = 0;
+        at.next_pair(p);
     }
     // copies that were asked for and not used (a wait that ran out) land before the block ends: the stages from
     // st on are in the current phase, those before it one further
@@ -814,8 +818,8 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 32 * WPR) k_join(const KParam
 // The shapes of a launch: warps and blocks at once as registers and the rings allow.
 template <int NG, int NT> struct Shape {
     static constexpr int W = 4;
-    static constexpr int NS = NG == 2 ? 4 : NG == 4 ? 3 : 2;
-    static constexpr int MB = NG == 2 ? (NT == 1 ? 4 : 2) : NG == 4 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 2 : 2);
+    static constexpr int NS = NG == 2 ? 4 : NG == 4 && NT == 2 ? 3 : 2;
+    static constexpr int MB = NG == 2 ? (NT == 1 ? 4 : 2) : NG == 4 && NT == 1 ? 3 : 2;
     static constexpr size_t smem = (size_t)W * NS * 1280 * NG + W * NS * 8;
     static_assert(smem <= 227 * 1024 / MB - 1024, "");
     static constexpr int shares = MB * W;                         // of an SM
