@@ -12,6 +12,10 @@
 // K blocks cut into equal shares, so every SM streams the same bytes.  A cut tile's CTAs leave their
 // int32 partials in the workspace and count themselves in; the last to arrive adds them: integer sums,
 // so the order does not matter, and nobody waits.
+//
+// PAIR: two CTAs of a cluster make one tile of 256 channels (cta_group::2): each holds 128 channels' rows and
+// half of the tokens' rows, so a K block brings 32 KB an SM into shared memory in place of 48 KB (BN = 256),
+// and the MMA reads as much less of it.  The even CTA issues for both.
 #include <new>
 #include "spffn_umma.cuh"
 #include "../../include/spffn_block.h"
@@ -24,6 +28,9 @@ using namespace um;
 constexpr int kTM = 128, kBK = 128, kThreads = 320, kMaxSt = 12;
 constexpr int kEpiThreads = 256;      // eight epilogue warps: two for each 32 lanes of TMEM, half the columns each
 constexpr int kGroupN = 8;            // channel tiles that share a stretch of the tile order
+#ifndef PAIR_MIN
+#define PAIR_MIN 96
+#endif
 constexpr int kMinBlocks = 4;         // K blocks of a share, at least
 constexpr size_t kSmem = 227 * 1024;
 
@@ -35,6 +42,7 @@ struct MParams {
     int64_t ldy;
     int T, N;
     int kblocks, n_tiles, t_tiles, bn, stages;
+    int units;                        // CTAs, or pairs of them
     int whole;                        // tiles per CTA that are dealt whole
     int cut_base, cut_tiles;          // the tiles that are cut, in line
     int4* partial;                    // [2 grid][bn / 4][128 rows] of 4 columns
@@ -48,16 +56,17 @@ struct Walk {
     long long pos, end;
     int w = 0, cur, stop;             // tiles of the line still to come, from the last to the first
     int tile, k0, k1, cut;            // cut: index of the tile in the line, -1 for a whole one
-    __device__ __forceinline__ explicit Walk(const MParams& p) {
+    int unit;
+    __device__ __forceinline__ Walk(const MParams& p, int u) : unit(u) {
         const long long total = (long long)p.cut_tiles * p.kblocks;
-        pos = total * blockIdx.x / gridDim.x;
-        end = total * (blockIdx.x + 1) / gridDim.x;
+        pos = total * u / p.units;
+        end = total * (u + 1) / p.units;
         cur = pos < end ? (int)((end - 1) / p.kblocks) : -1;
         stop = pos < end ? (int)(pos / p.kblocks) : 0;
     }
     __device__ __forceinline__ bool next(const MParams& p) {
         if (w < p.whole) {
-            tile = w++ * gridDim.x + blockIdx.x;
+            tile = w++ * p.units + unit;
             k0 = 0;
             k1 = p.kblocks;
             cut = -1;
@@ -81,7 +90,16 @@ __device__ __forceinline__ void tile_at(const MParams& p, int tile, int& nt, int
     tt = r / gn;
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void umma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+    if constexpr (PAIR) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accum));
+        return;
+    }
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
@@ -96,6 +114,36 @@ __device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int* r) {
         : "r"(taddr));
 }
 
+// a tile of this CTA's, its arrival counted at the even CTA's barrier
+__device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(s32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// what was issued so far is done: tell this CTA's barrier, or both CTAs' at the same place
+template <bool PAIR> __device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(s32(bar)),
+                     "h"((uint16_t)3) : "memory");
+    else ucommit(bar);
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+template <bool PAIR> __device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(slot)), "r"(512u));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(slot)), "r"(512u));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+}
+template <bool PAIR> __device__ __forceinline__ void tmem_free(uint32_t tmem) {
+    if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
 // the epilogue warps' barrier, and whether all of them say so: they leave a wait together or not at all
 __device__ __forceinline__ bool epi_all(bool ok) {
     uint32_t r;
@@ -107,12 +155,13 @@ __device__ __forceinline__ bool epi_all(bool ok) {
     return r != 0;
 }
 
-template <typename D>
+template <typename D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MParams p) {
     extern __shared__ __align__(1024) char smem[];
     char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem) + 1023) & ~uintptr_t(1023));
     const int S = p.stages, BN = p.bn;
-    const uint32_t stage_bytes = kTM * kBK + BN * kBK;
+    const int AR = PAIR ? BN / 2 : BN;     // token rows of this CTA
+    const uint32_t stage_bytes = kTM * kBK + AR * kBK;
     uint64_t* full = reinterpret_cast<uint64_t*>(base + S * stage_bytes);
     uint64_t* empty = full + kMaxSt;
     uint64_t* tfull = empty + kMaxSt;      // [2]
@@ -122,20 +171,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
     int* s_last = reinterpret_cast<int*>(tempty + 4);
     uint64_t* done = tempty + 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, rank = PAIR ? blockIdx.x & 1 : 0;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) { ub_init(&full[i], 1); ub_init(&empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { ub_init(&tfull[i], 1); ub_init(&tempty[i], kEpiThreads / 32); }
+        for (int i = 0; i < 2; ++i) { ub_init(&tfull[i], 1); ub_init(&tempty[i], (PAIR ? 2 : 1) * kEpiThreads / 32); }
         ub_init(done, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(tmem_slot)), "r"(512u));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
+    if (warp == 1) tmem_alloc<PAIR>(tmem_slot);
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();   // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     // programmatic dependent launch: what comes before overlaps the previous kernel's end
@@ -146,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
         if (lane == 0) {                   // ------------------------------------ TMA producer
             int st = 0, ph = 0;
             uint32_t issued = 0, last_ph = 0;
-            Walk w(p);
+            Walk w(p, unit);
             bool ok = true;
             while (ok && w.next(p)) {
                 int nt, tt;
@@ -154,26 +202,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
                 for (int kb = w.k0; kb < w.k1; ++kb) {
                     if (!ub_wait(&empty[st], ph ^ 1, abort_flag, p.err)) { ok = false; break; }
                     char* sw = base + st * stage_bytes;
-                    ub_expect(&full[st], stage_bytes);
-                    tma_2d(sw, &p.mW, kb * kBK, nt * kTM, &full[st]);
-                    tma_2d(sw + kTM * kBK, &p.mA, kb * kBK, tt * BN, &full[st]);
+                    if constexpr (PAIR) {
+                        const uint32_t bar = cluster_map(s32(&full[st]), 0);
+                        if (rank == 0) ub_expect(&full[st], 2 * stage_bytes);
+                        tma_2d_pair(sw, &p.mW, kb * kBK, nt * 2 * kTM + rank * kTM, bar);
+                        tma_2d_pair(sw + kTM * kBK, &p.mA, kb * kBK, tt * BN + rank * AR, bar);
+                    } else {
+                        ub_expect(&full[st], stage_bytes);
+                        tma_2d(sw, &p.mW, kb * kBK, nt * kTM, &full[st]);
+                        tma_2d(sw + kTM * kBK, &p.mA, kb * kBK, tt * BN, &full[st]);
+                    }
                     issued |= 1u << st;
                     last_ph = (last_ph & ~(1u << st)) | ((uint32_t)ph << st);
                     if (++st == S) { st = 0; ph ^= 1; }
                 }
             }
-            // a copy that nobody consumed (an abort) has to land before the block ends
-            for (int i = 0; i < S; ++i)
-                if ((issued >> i) & 1u) {
-                    const unsigned long long t0 = now_ns();
-                    while (!ub_try(&full[i], (last_ph >> i) & 1u) && now_ns() - t0 < 20000000ull) {}
-                }
+            // the last fill of every stage has been consumed (of a pair: no arrival from the even CTA is still on
+            // its way), or, after an abort, has landed; of a pair the even CTA sees both CTAs' copies, and the
+            // other one stays until the cluster's last barrier
+            for (int i = 0; i < S; ++i) {
+                if (!((issued >> i) & 1u)) continue;
+                const uint32_t parity = (last_ph >> i) & 1u;
+                if (ub_wait(&empty[i], parity, abort_flag, p.err) || rank) continue;
+                const unsigned long long t0 = now_ns();
+                while (!ub_try(&full[i], parity) && now_ns() - t0 < 20000000ull) {}
+            }
         }
     } else if (warp == 1) {
-        if (lane == 0) {                   // ------------------------------------ MMA
-            const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kTM >> 4) << 24);
+        if (lane == 0 && rank == 0) {      // ------------------------------------ MMA
+            const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)((PAIR ? 2 : 1) * kTM >> 4) << 24);
             int st = 0, ph = 0, ab = 0, aph = 0;
-            Walk w(p);
+            Walk w(p, unit);
             bool ok = true;
             while (ok && w.next(p)) {
                 if (!ub_wait(&tempty[ab], aph ^ 1, abort_flag, p.err)) break;
@@ -185,16 +244,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
                     const uint32_t sw = s32(base + st * stage_bytes), sa = sw + kTM * kBK;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        umma_i8(d, sdesc(sw + k * 32u, 1u, 64u), sdesc(sa + k * 32u, 1u, 64u), idesc, kb > w.k0 || k > 0);
-                    ucommit(&empty[st]);
+                        umma_i8<PAIR>(d, sdesc(sw + k * 32u, 1u, 64u), sdesc(sa + k * 32u, 1u, 64u), idesc, kb > w.k0 || k > 0);
+                    mma_commit<PAIR>(&empty[st]);
                     if (++st == S) { st = 0; ph ^= 1; }
                 }
                 if (!ok) break;
-                ucommit(&tfull[ab]);
+                mma_commit<PAIR>(&tfull[ab]);
                 if (++ab == 2) { ab = 0; aph ^= 1; }
             }
             if (*abort_flag) {             // what was issued ends before the block does
-                ucommit(done);
+                mma_commit<PAIR>(done);
                 const unsigned long long t0 = now_ns();
                 while (!ub_try(done, 0) && now_ns() - t0 < 20000000ull) {}
             }
@@ -202,11 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
     } else {                               // ---------------------------------------- epilogue
         const int quad = warp & 3, row = quad * 32 + lane, side = (warp - 2) >> 2;
         int ab = 0, aph = 0;
-        Walk w(p);
+        Walk w(p, unit);
         while (w.next(p)) {
             int nt, tt;
             tile_at(p, w.tile, nt, tt);
-            const int n = nt * kTM + row;
+            const int n = (PAIR ? 2 * nt + rank : nt) * kTM + row;
             const bool in = n < p.N;
             const float ws = in ? __ldg(p.w_scale + n) : 0.f;
             const float bias = in && p.bias ? DT<D>::f(static_cast<const D*>(p.bias)[n]) : 0.f;
@@ -221,11 +280,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
             }
             int c_first = 0, c_last = -1;  // the CTAs of a cut tile
             uint32_t others = 0;           // how many there are beside this one
+            uint32_t* ticket = p.tickets + (w.cut < 0 ? 0 : PAIR ? 2 * w.cut + rank : w.cut);
+            constexpr int kSides = PAIR ? 2 : 1;
             bool finish = true;
             if (w.cut >= 0) {
                 const long long total = (long long)p.cut_tiles * p.kblocks, lo = (long long)w.cut * p.kblocks;
-                c_first = (int)(((lo + 1) * gridDim.x - 1) / total);
-                c_last = (int)(((lo + p.kblocks) * gridDim.x - 1) / total);
+                c_first = (int)(((lo + 1) * p.units - 1) / total);
+                c_last = (int)(((lo + p.kblocks) * p.units - 1) / total);
                 others = (uint32_t)(c_last - c_first);
             }
             if (!epi_all(ub_wait(&tfull[ab], aph, abort_flag, p.err))) break;
@@ -233,11 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
             const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(ab * 256);
             if (w.cut >= 0) {
                 // where all the others are in, this one's part need not leave TMEM
-                if (threadIdx.x == 64) *s_last = ld_acquire_u32(&p.tickets[w.cut]) == others;
+                if (threadIdx.x == 64) *s_last = ld_acquire_u32(ticket) == others;
                 epi_all(true);
                 finish = *s_last;
                 if (!finish) {
-                    int4* mine = p.partial + (size_t)(2 * blockIdx.x + (w.k0 == 0)) * (BN / 4) * kTM + row;
+                    int4* mine = p.partial + (size_t)((2 * unit + (w.k0 == 0)) * kSides + rank) * (BN / 4) * kTM + row;
                     for (int c0 = 16 * side; c0 < cols; c0 += 32) {
                         int v[16];
                         tmem_ld16i(taddr + c0, v);
@@ -247,11 +308,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
                             __stcg(mine + (c0 / 4 + c) * kTM, make_int4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
                     }
                     epi_all(true);
-                    if (threadIdx.x == 64) *s_last = atom_acq_rel_add_u32(&p.tickets[w.cut], 1u) == others;
+                    if (threadIdx.x == 64) *s_last = atom_acq_rel_add_u32(ticket, 1u) == others;
                     epi_all(true);
                     finish = *s_last;
                 }
-                if (finish && threadIdx.x == 64) p.tickets[w.cut] = 0;      // for the next call
+                if (finish && threadIdx.x == 64) *ticket = 0;      // for the next call
             }
             if (finish) {
                 D* y = static_cast<D*>(p.y) + (int64_t)t0 * p.ldy + n;
@@ -264,9 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
                     tmem_wait_ld();
 #pragma unroll 2
                     for (int o = c_first; o <= c_last; ++o) {
-                        if (o == (int)blockIdx.x) continue;
+                        if (o == unit) continue;
                         // its piece of this tile starts at 0 only if it is the first
-                        const int4* from = p.partial + ((size_t)(2 * o + (o == c_first ? 1 : 0)) * (BN / 4) + c0 / 4) * kTM + row;
+                        const int4* from = p.partial + ((size_t)((2 * o + (o == c_first ? 1 : 0)) * kSides + rank) * (BN / 4) + c0 / 4) * kTM + row;
                         int4 u[8];
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
@@ -295,7 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) ub_arrive(&tempty[ab]);
+            if (lane == 0) {
+                if (rank == 0) ub_arrive(&tempty[ab]);
+                else arrive_at(cluster_map(s32(&tempty[ab]), 0));
+            }
             if (++ab == 2) { ab = 0; aph ^= 1; }
         }
     }
@@ -303,7 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+    if constexpr (PAIR) cluster_sync_all();   // nothing of the other CTA's is still on its way here
+    if (warp == 1) tmem_free<PAIR>(tmem);
 }
 
 // [rows][cols] bytes of row stride `ld`, box {128, box_rows}, 128-byte swizzle
@@ -323,8 +388,8 @@ struct Layout8 {
 Layout8 layout8(const spffn_mm8_config& c, int sms) {
     Layout8 l;
     l.tickets = kCtlBytes;
-    l.partial = align_up(l.tickets + (size_t)2 * sms * sizeof(uint32_t), 256);
-    l.total = l.partial + (size_t)2 * sms * std::min(256, round16(c.max_tokens)) * kTM * sizeof(int);
+    l.partial = align_up(l.tickets + (size_t)2 * sms * sizeof(uint32_t), 256);   // pairs: two a tile of half as many
+    l.total = l.partial + (size_t)2 * sms * std::min(256, (c.max_tokens + 31) / 32 * 32) * kTM * sizeof(int);
     return l;
 }
 
@@ -394,35 +459,43 @@ spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda,
     p.T = T;
     p.N = c.N;
     p.kblocks = (c.K + kBK - 1) / kBK;
-    p.n_tiles = (c.N + kTM - 1) / kTM;
     p.t_tiles = (T + 255) / 256;
     p.bn = round16((T + p.t_tiles - 1) / p.t_tiles);
-    const size_t stage = (size_t)(kTM + p.bn) * kBK, extra = 1024 + (2 * kMaxSt + 8) * 8;
+    // pairs of CTAs where the MMA's reads of shared memory bound a tile, from PAIR_MIN tokens on
+    const bool pair = p.bn >= PAIR_MIN && c.N > kTM;
+    if (pair) p.bn = (p.bn + 31) / 32 * 32;
+    const int rows = pair ? p.bn / 2 : p.bn;         // token rows of a CTA
+    p.n_tiles = (c.N + (pair ? 2 : 1) * kTM - 1) / ((pair ? 2 : 1) * kTM);
+    const size_t stage = (size_t)(kTM + rows) * kBK, extra = 1024 + (2 * kMaxSt + 10) * 8;
     p.stages = (int)std::min<size_t>(kMaxSt, (kSmem - extra) / stage);
     // whole tiles while two full waves are left, the rest in equal shares
     const long long tiles = (long long)p.n_tiles * p.t_tiles, total = tiles * p.kblocks;
-    const int grid = (int)std::min<long long>(ctx->sms, std::max<long long>(tiles, total / kMinBlocks));
-    p.whole = tiles % grid == 0 ? (int)(tiles / grid) : (int)std::max<long long>(0, tiles / grid - 1);
-    p.cut_base = p.whole * grid;
+    p.units = (int)std::min<long long>(pair ? ctx->sms / 2 : ctx->sms, std::max<long long>(tiles, total / kMinBlocks));
+    p.whole = tiles % p.units == 0 ? (int)(tiles / p.units) : (int)std::max<long long>(0, tiles / p.units - 1);
+    p.cut_base = p.whole * p.units;
     p.cut_tiles = (int)(tiles - p.cut_base);
     p.partial = reinterpret_cast<int4*>(ctx->ws + ctx->lay.partial);
     p.tickets = reinterpret_cast<uint32_t*>(ctx->ws + ctx->lay.tickets);
     p.err = reinterpret_cast<uint32_t*>(ctx->ws);
-    if (!map_i8(&p.mW, ctx->w.W, c.N, c.K, c.K, kTM) || !map_i8(&p.mA, A, T, c.K, lda, p.bn)) return SPFFN_ERR_UNSUPPORTED;
+    if (!map_i8(&p.mW, ctx->w.W, c.N, c.K, c.K, kTM) || !map_i8(&p.mA, A, T, c.K, lda, rows)) return SPFFN_ERR_UNSUPPORTED;
     const size_t smem = p.stages * stage + extra;
-    auto kern = c.dtype == SPFFN_BF16 ? k_mm8<__nv_bfloat16> : k_mm8<__half>;
+    auto kern = c.dtype == SPFFN_BF16 ? (pair ? k_mm8<__nv_bfloat16, true> : k_mm8<__nv_bfloat16, false>)
+                                      : (pair ? k_mm8<__half, true> : k_mm8<__half, false>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return record_cuda(e);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = dim3((unsigned)(pair ? 2 * p.units : p.units));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = pair ? 2 : 1;
     return record_cuda(cudaLaunchKernelEx(&cfg, kern, p));
 }
 
