@@ -41,6 +41,7 @@ struct MParams {
     void* y;
     int64_t ldy;
     int T, N;
+    int two;                          // y in whole pairs of channels
     int kblocks, n_tiles, t_tiles, bn, stages;
     int units;                        // CTAs, or pairs of them
     int whole;                        // tiles per CTA that are dealt whole
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 3);
     int* s_last = reinterpret_cast<int*>(tempty + 4);
     uint64_t* done = tempty + 5;
+    float* s_scale = reinterpret_cast<float*>(tempty + 6);   // [2][256]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, rank = PAIR ? blockIdx.x & 1 : 0;
 
@@ -270,30 +272,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
             const float ws = in ? __ldg(p.w_scale + n) : 0.f;
             const float bias = in && p.bias ? DT<D>::f(static_cast<const D*>(p.bias)[n]) : 0.f;
             const int t0 = tt * BN, cols = min(BN, p.T - t0);
-            // pieces of 16 columns, the two warps of a quadrant take turns; lane c holds the scale of
-            // the c-th of the 32 columns that the warp finishes at a time
-            float as[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int col = 16 * side + 64 * i + (lane & 15) + 2 * (lane & 16);
-                as[i] = col < cols ? __ldg(p.a_scale + t0 + col) : 0.f;
-            }
-            int c_first = 0, c_last = -1;  // the CTAs of a cut tile
+            // the tokens' scales, read back four at a time; the barrier below makes them visible, and two buffers
+            // keep the tile before
+            float* as = s_scale + 256 * ab;
+            const int et = threadIdx.x - 64;
+            as[et] = et < cols ? __ldg(p.a_scale + t0 + et) : 0.f;
+            int c_first = 0, c_last = -1;  // the CTAs (or pairs) of a cut tile
             uint32_t others = 0;           // how many there are beside this one
             uint32_t* ticket = p.tickets + (w.cut < 0 ? 0 : PAIR ? 2 * w.cut + rank : w.cut);
             constexpr int kSides = PAIR ? 2 : 1;
             bool finish = true;
+            // pieces of 16 columns, the two warps of a quadrant take turns; a warp finishes 32 columns at a time
+            auto part_of = [&](int o, int c0) {      // its piece of this tile starts at 0 only if it is the first
+                return p.partial + ((size_t)((2 * o + (o == c_first)) * kSides + rank) * (BN / 4) + c0 / 4) * kTM + row;
+            };
+            int4 u[8];                     // of the only other part, the next 32 columns ahead
+            auto fetch = [&](int o, int c0) {
+                const int4* from = part_of(o, c0);
+                const bool two = c0 + 32 < cols;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    u[c] = c0 < cols ? __ldcg(from + c * kTM) : make_int4(0, 0, 0, 0);
+                    u[c + 4] = two ? __ldcg(from + (c + 8) * kTM) : make_int4(0, 0, 0, 0);
+                }
+            };
+            int other = -1;                // set where there is only one
             if (w.cut >= 0) {
                 const long long total = (long long)p.cut_tiles * p.kblocks, lo = (long long)w.cut * p.kblocks;
                 c_first = (int)(((lo + 1) * p.units - 1) / total);
                 c_last = (int)(((lo + p.kblocks) * p.units - 1) / total);
                 others = (uint32_t)(c_last - c_first);
+                if (others == 1) other = c_first == unit ? c_last : c_first;
+                // where all the others are in, this one's part need not leave TMEM, and theirs can be read meanwhile
+                if (threadIdx.x == 64) *s_last = ld_acquire_u32(ticket) == others;
+                epi_all(true);
+                finish = *s_last;
+                if (finish && other >= 0) fetch(other, 16 * side);
             }
             if (!epi_all(ub_wait(&tfull[ab], aph, abort_flag, p.err))) break;
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(ab * 256);
-            if (w.cut >= 0) {
-                // where all the others are in, this one's part need not leave TMEM
+            if (!finish) {
                 if (threadIdx.x == 64) *s_last = ld_acquire_u32(ticket) == others;
                 epi_all(true);
                 finish = *s_last;
@@ -312,28 +331,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
                     epi_all(true);
                     finish = *s_last;
                 }
-                if (finish && threadIdx.x == 64) *ticket = 0;      // for the next call
+                if (finish && other >= 0) fetch(other, 16 * side);
             }
+            if (w.cut >= 0 && finish && threadIdx.x == 64) *ticket = 0;      // for the next call
             if (finish) {
                 D* y = static_cast<D*>(p.y) + (int64_t)t0 * p.ldy + n;
-                // two pieces at a time, so that a cut tile's partials come 8 loads deep
                 for (int c0 = 16 * side; c0 < cols; c0 += 64) {
                     int v[32];
                     const bool two = c0 + 32 < cols;
                     tmem_ld16i(taddr + c0, v);
                     if (two) tmem_ld16i(taddr + c0 + 32, v + 16);
                     tmem_wait_ld();
-#pragma unroll 2
-                    for (int o = c_first; o <= c_last; ++o) {
-                        if (o == unit) continue;
-                        // its piece of this tile starts at 0 only if it is the first
-                        const int4* from = p.partial + ((size_t)((2 * o + (o == c_first ? 1 : 0)) * kSides + rank) * (BN / 4) + c0 / 4) * kTM + row;
-                        int4 u[8];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            u[c] = __ldcg(from + c * kTM);
-                            u[c + 4] = two ? __ldcg(from + (c + 8) * kTM) : make_int4(0, 0, 0, 0);
-                        }
+                    if (other >= 0) {
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             v[4 * c] += u[c].x;
@@ -341,16 +350,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
                             v[4 * c + 2] += u[c].z;
                             v[4 * c + 3] += u[c].w;
                         }
-                    }
-                    const float asc = as[0];
-                    as[0] = as[1];
-                    as[1] = as[2];
-                    as[2] = as[3];
+                        fetch(other, c0 + 64);
+                    } else {
+                        for (int o = c_first; o <= c_last; ++o) {
+                            if (o == unit) continue;
+                            fetch(o, c0);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const int col = c0 + (c & 15) + 2 * (c & 16);
-                        const float f = __shfl_sync(0xffffffffu, asc, c) * ws;
-                        if (in && col < cols) y[(int64_t)col * p.ldy] = DT<D>::r((float)v[c] * f + bias);
+                            for (int c = 0; c < 8; ++c) {
+                                v[4 * c] += u[c].x;
+                                v[4 * c + 1] += u[c].y;
+                                v[4 * c + 2] += u[c].z;
+                                v[4 * c + 3] += u[c].w;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (h && !two) break;
+                        const int b0 = c0 + 32 * h;
+                        float f[16];
+#pragma unroll
+                        for (int c = 0; c < 16; c += 4) {
+                            const float4 a = *reinterpret_cast<const float4*>(as + b0 + c);
+                            f[c] = fmaf((float)v[16 * h + c], a.x * ws, bias);
+                            f[c + 1] = fmaf((float)v[16 * h + c + 1], a.y * ws, bias);
+                            f[c + 2] = fmaf((float)v[16 * h + c + 2], a.z * ws, bias);
+                            f[c + 3] = fmaf((float)v[16 * h + c + 3], a.w * ws, bias);
+                        }
+                        D* to = y + (int64_t)b0 * p.ldy;
+                        if (p.two) {
+                            // a lane and its neighbour swap, so that each stores two channels of every other column
+                            const int odd = lane & 1;
+                            uint32_t* to2 = reinterpret_cast<uint32_t*>(to + (int64_t)odd * p.ldy - odd);
+#pragma unroll
+                            for (int c = 0; c < 16; c += 2) {
+                                const float got = __shfl_xor_sync(0xffffffffu, odd ? f[c] : f[c + 1], 1);
+                                const D pr[2] = {DT<D>::r(odd ? got : f[c]), DT<D>::r(odd ? f[c + 1] : got)};
+                                if (in && b0 + c + odd < cols) *to2 = *reinterpret_cast<const uint32_t*>(pr);
+                                to2 += p.ldy;             // two rows, in pairs of channels
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                if (in && b0 + c < cols) *to = DT<D>::r(f[c]);
+                                to += p.ldy;
+                            }
+                        }
                     }
                 }
             }
@@ -458,6 +503,7 @@ spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda,
     p.ldy = ldy;
     p.T = T;
     p.N = c.N;
+    p.two = c.N % 2 == 0 && ldy % 2 == 0 && aligned_to(y, 4);
     p.kblocks = (c.K + kBK - 1) / kBK;
     p.t_tiles = (T + 255) / 256;
     p.bn = round16((T + p.t_tiles - 1) / p.t_tiles);
@@ -466,7 +512,7 @@ spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda,
     if (pair) p.bn = (p.bn + 31) / 32 * 32;
     const int rows = pair ? p.bn / 2 : p.bn;         // token rows of a CTA
     p.n_tiles = (c.N + (pair ? 2 : 1) * kTM - 1) / ((pair ? 2 : 1) * kTM);
-    const size_t stage = (size_t)(kTM + rows) * kBK, extra = 1024 + (2 * kMaxSt + 10) * 8;
+    const size_t stage = (size_t)(kTM + rows) * kBK, extra = 1024 + (2 * kMaxSt + 10) * 8 + 2 * 256 * sizeof(float);
     p.stages = (int)std::min<size_t>(kMaxSt, (kSmem - extra) / stage);
     // whole tiles while two full waves are left, the rest in equal shares
     const long long tiles = (long long)p.n_tiles * p.t_tiles, total = tiles * p.kblocks;
