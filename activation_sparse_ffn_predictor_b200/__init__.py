@@ -514,12 +514,11 @@ def _rows(t, what: str, dtype, T=None, d=None):
 
 
 def _vector(t, what: str, dtype, n: int):
-    if t.shape != (n,):
-        raise ValueError("%s: expected shape [%d], got %s" % (what, n, tuple(t.shape)))
+    if t.dtype is dtype and t.shape == (n,) and t.is_contiguous():
+        return
     if t.dtype is not dtype:
         raise TypeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
-    if n > 1 and t.stride(0) != 1:
-        raise ValueError("%s must be contiguous" % what)
+    raise ValueError("%s: expected a contiguous [%d], got %s" % (what, n, tuple(t.shape)))
 
 
 def _ptr(t):
@@ -716,9 +715,9 @@ class KvCache4:
 
     def _heads(self, t, what: str, T: int, heads: int):
         """Row stride of [T, heads, dh] (or [T, heads * dh]) whose rows are contiguous."""
-        if len(t.shape) == 3:
+        if t.dim() == 3:
             ld, head, one = t.stride()
-            if t.shape != (T, heads, self.dh) or one != 1 or (heads > 1 and head != self.dh):
+            if t.shape != (T, heads, self.dh) or one != 1 or (head != self.dh and heads > 1):
                 raise ValueError("%s: expected [%d, %d, %d] with contiguous rows, got %s, strides %s" % (
                     what, T, heads, self.dh, tuple(t.shape), t.stride()))
             if t.dtype is not self.dtype:

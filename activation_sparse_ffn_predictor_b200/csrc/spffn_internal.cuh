@@ -1,6 +1,7 @@
 // Internal definitions shared by the spffn kernels and the C-ABI glue.
 #pragma once
 #include <algorithm>
+#include <atomic>
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
@@ -160,6 +161,15 @@ inline bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uin
 inline bool on_device(int device) {
     int now = -1;
     return cudaGetDevice(&now) == cudaSuccess && now == device;
+}
+// allow a kernel its dynamic shared memory, once for each device (`ready` is the kernel's own)
+template <typename K>
+inline cudaError_t allow_smem(K kern, size_t bytes, int device, std::atomic<uint64_t>& ready) {
+    const uint64_t bit = 1ull << (device & 63);
+    if (device < 64 && (ready.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 // read and clear a latched error word at the head of a workspace (synchronises the stream)
 inline spffn_status take_device_error(uint32_t* err, uint32_t* code, void* stream) {

@@ -13,8 +13,13 @@
 // bits of a halfword is the fp16 subnormal n 2^-24 and in bits 4..7 n 2^-20: two ANDs turn a word
 // into operands, no conversion; the 2^-24 and the 16 are undone on scores, outputs and q.
 // q is brought to [2^9, 2^10) by a power of two per row (exact), so a bf16 q fits fp16; the sums of
-// q_g enter as a high and a low half.  Probabilities are rounded to fp16 once alone and once times
-// the step (2^-11 each, against 2^-9 or 2^-12 of the output's own rounding); they are kept as
+// q_g enter as a high and a low half.  Probabilities times steps are rounded to fp16.  Where the output
+// is bf16 (its own rounding is 2^-8) the probability is rounded before as well, and the codes of V enter
+// as 0..15, whose sum the zeros take back.  Where it is fp16 (2^-11) a second half carries what the first
+// rounding lost, so that one is left, and V's codes enter as n - 8 (one fp16 operation a pair): the matrix
+// instructions cut their sums off rather than round them, and over 100,000 positions that showed as 5e-4
+// of the small difference of two large sums.  Measured against 64 bits: 2.9e-4, of which the output's
+// rounding is 2.1e-4; 6e-4 the other way, and 4 us of 39 faster.  Probabilities are kept as
 // 2^(7 - R) p and up to 2^8 more before the reference moves, R an exponent above every V step seen, so
 // that p s stays in fp16's range.
 //
@@ -26,6 +31,7 @@
 // k_join adds them in their order.  (Measured and not kept: half shares that warps take as they come,
 // 137 us against 127 at 32 sequences of 1400 positions, 72 heads; blocks that go through a share together
 // and join through shared memory, with the last block to arrive joining the cut heads, 156 us.)
+#include <type_traits>
 #include "spffn_umma.cuh"
 #include "spffn_kv4.cuh"
 
@@ -173,6 +179,7 @@ template <typename T, int NG, int NT, int W, int NS, int MB>
 __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
     using L = Blk<NG>;
     constexpr int R = 8 * NT, DH = 32 * NG, kSnap = 2;
+    constexpr bool kFine = std::is_same<T, __half>::value;
     constexpr uint32_t kTile = 2 * L::kBytes;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring = smem;                                         // [W][NS][kTile]
@@ -580,7 +587,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                     vexp = vnew;
                 }
                 // probabilities, turned into the second operand of the output's product
-                uint32_t pb[2][NT][2];
+                uint32_t pb[2][NT][2], pl[kFine ? 2 : 1][NT][2];   // and what rounding them lost
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -591,8 +598,14 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                             pr[i] = ex2(sc[j][t][i] - fmaxf(s.off[t][i & 1], -3e38f));
                             s.l[t][i & 1] += pr[i];
                         }
-                        pb[j][t][0] = transpose8(pack2(pr[0], pr[1]));
-                        pb[j][t][1] = transpose8(pack2(pr[2], pr[3]));
+                        const uint32_t h0 = pack2(pr[0], pr[1]), h1 = pack2(pr[2], pr[3]);
+                        pb[j][t][0] = transpose8(h0);
+                        pb[j][t][1] = transpose8(h1);
+                        if constexpr (kFine) {
+                            const float2 f0 = __half22float2(as_h2(h0)), f1 = __half22float2(as_h2(h1));
+                            pl[j][t][0] = transpose8(pack2(pr[0] - f0.x, pr[1] - f0.y));
+                            pl[j][t][1] = transpose8(pack2(pr[2] - f1.x, pr[3] - f1.y));
+                        }
                     }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -604,6 +617,12 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                     lds<NG>(s1, blk + L::kVs + 16 * NG + c * 4 * NG);
                     uint32_t z0 = *reinterpret_cast<const uint32_t*>(blk + L::kVz + c * 4 * NG + 4 * (r & (NG - 1)));
                     uint32_t z1 = *reinterpret_cast<const uint32_t*>(blk + L::kVz + 16 * NG + c * 4 * NG + 4 * (r & (NG - 1)));
+                    if constexpr (kFine) {                        // zeros for codes around 8
+                        const int at_s = L::kVs + c * 4 * NG + 4 * (r & (NG - 1));
+                        const __half2 eight = __float2half2_rn(8.f);
+                        z0 = as_u(__hfma2(as_h2(*reinterpret_cast<const uint32_t*>(blk + at_s)), eight, as_h2(z0)));
+                        z1 = as_u(__hfma2(as_h2(*reinterpret_cast<const uint32_t*>(blk + at_s + 16 * NG)), eight, as_h2(z1)));
+                    }
                     if (r >= NG) z0 = z1 = 0u;
 #pragma unroll
                     for (int t = 0; t < NT; ++t) mma(oz[t], z0, 0u, z1, 0u, pb[j][t][0], pb[j][t][1]);
@@ -612,8 +631,13 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                         uint32_t b0[NT], b1[NT];
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            b0[t] = as_u(__hmul2(as_h2(pb[j][t][0]), as_h2(s0[g])));
-                            b1[t] = as_u(__hmul2(as_h2(pb[j][t][1]), as_h2(s1[g])));
+                            if constexpr (kFine) {
+                                b0[t] = as_u(__hfma2(as_h2(pb[j][t][0]), as_h2(s0[g]), __hmul2(as_h2(pl[j][t][0]), as_h2(s0[g]))));
+                                b1[t] = as_u(__hfma2(as_h2(pb[j][t][1]), as_h2(s1[g]), __hmul2(as_h2(pl[j][t][1]), as_h2(s1[g]))));
+                            } else {
+                                b0[t] = as_u(__hmul2(as_h2(pb[j][t][0]), as_h2(s0[g])));
+                                b1[t] = as_u(__hmul2(as_h2(pb[j][t][1]), as_h2(s1[g])));
+                            }
                         }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -621,9 +645,16 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                             const int wd = g >> 1, by = 2 * (g & 1) + i;
                             const uint32_t sel = (uint32_t)(by | (by << 4) | ((4 + by) << 8) | ((4 + by) << 12));
                             const uint32_t a = __byte_perm(w0[wd], w0[NG / 2 + wd], sel), b = __byte_perm(w1[wd], w1[NG / 2 + wd], sel);
+                            uint32_t a0 = a & 0x000f000fu, a1 = a & 0x00f000f0u, a2 = b & 0x000f000fu, a3 = b & 0x00f000f0u;
+                            if constexpr (kFine) {                // 1024 + n and 1024 + 16 n, brought to n - 8
+                                const __half2 m1032 = __float2half2_rn(-1032.f), m72 = __float2half2_rn(-72.f), sixteenth = __float2half2_rn(0.0625f);
+                                a0 = as_u(__hadd2(as_h2(a0 | 0x64006400u), m1032));
+                                a1 = as_u(__hfma2(as_h2(a1 | 0x64006400u), sixteenth, m72));
+                                a2 = as_u(__hadd2(as_h2(a2 | 0x64006400u), m1032));
+                                a3 = as_u(__hfma2(as_h2(a3 | 0x64006400u), sixteenth, m72));
+                            }
 #pragma unroll
-                            for (int t = 0; t < NT; ++t)
-                                mma(s.o[2 * g + i][t], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u, b0[t], b1[t]);
+                            for (int t = 0; t < NT; ++t) mma(s.o[2 * g + i][t], a0, a1, a2, a3, b0[t], b1[t]);
                         }
                     }
                 }
@@ -649,8 +680,8 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                     const float z = __shfl_sync(0xffffffffu, oz[t][i], 4 * g + c);
 #pragma unroll
                     for (int d = 2 * g; d < 2 * g + 2; ++d) {
-                        s.o[d][t][i] = fmaf(s.o[d][t][i], 16777216.f, z);
-                        s.o[d][t][i + 2] = fmaf(s.o[d][t][i + 2], 1048576.f, z);
+                        s.o[d][t][i] = kFine ? s.o[d][t][i] + z : fmaf(s.o[d][t][i], 16777216.f, z);
+                        s.o[d][t][i + 2] = kFine ? s.o[d][t][i + 2] + z : fmaf(s.o[d][t][i + 2], 1048576.f, z);
                     }
                 }
             }
@@ -849,7 +880,8 @@ template <typename T, int NG, int NT>
 cudaError_t go(const spffn_kv4_ctx& c, KParams p, cudaStream_t st) {
     using S = Shape<NG, NT>;
     auto kern = k_attend<T, NG, NT, S::W, S::NS, S::MB>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
+    static std::atomic<uint64_t> ready{0};                        // a bit a device
+    cudaError_t e = allow_smem(kern, S::smem, c.device, ready);
     if (e != cudaSuccess) return e;
     p.many = c.sms * S::shares;
     e = launch_chained(kern, (unsigned)(c.sms * S::MB), 32 * S::W, S::smem, p, st);

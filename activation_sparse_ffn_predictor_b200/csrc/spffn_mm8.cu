@@ -527,7 +527,8 @@ spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda,
     const size_t smem = p.stages * stage + extra;
     auto kern = c.dtype == SPFFN_BF16 ? (pair ? k_mm8<__nv_bfloat16, true> : k_mm8<__nv_bfloat16, false>)
                                       : (pair ? k_mm8<__half, true> : k_mm8<__half, false>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    static std::atomic<uint64_t> ready[4];              // a bit a device, for each of the four
+    const cudaError_t e = allow_smem(kern, kSmem, ctx->device, ready[(c.dtype == SPFFN_BF16 ? 2 : 0) + (pair ? 1 : 0)]);
     if (e != cudaSuccess) return record_cuda(e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pair ? 2 * p.units : p.units));
