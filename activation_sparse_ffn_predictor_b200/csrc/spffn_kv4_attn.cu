@@ -30,7 +30,10 @@
 // A head that lies inside a share is written out at once; the parts of a cut one go to the workspace and
 // k_join adds them in their order.  (Measured and not kept: half shares that warps take as they come,
 // 137 us against 127 at 32 sequences of 1400 positions, 72 heads; blocks that go through a share together
-// and join through shared memory, with the last block to arrive joining the cut heads, 156 us.)
+// and join through shared memory, with the last block to arrive joining the cut heads, 156 us; for many
+// query rows, blocks that unpack 64 positions into shared memory for 64 rows in the usual layout, rows as
+// M, 132 us against 138 at 256 new tokens over 8205 positions, 32 heads of 64 over 8: unpacking is a small
+// part there, arithmetic on scores and its latency the large one.)
 #include <type_traits>
 #include "spffn_umma.cuh"
 #include "spffn_kv4.cuh"
@@ -46,6 +49,7 @@ using um::ub_init;
 using um::ub_try;
 
 constexpr int kUnit = 32;             // positions of a unit
+constexpr int kSnap = 2;              // a cut as near as that to a head's end moves there
 constexpr int kHead = 1;              // what a head costs beside its units, in units: its q, its sums, its rows
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -175,28 +179,29 @@ __device__ __forceinline__ float2* part_sums(const KParams& p, int slot, int R, 
     return reinterpret_cast<float2*>(p.part + (size_t)2 * p.many * R * DH) + (size_t)slot * R;
 }
 
-template <typename T, int NG, int NT, int W, int NS, int MB>
-__global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
-    using L = Blk<NG>;
-    constexpr int R = 8 * NT, DH = 32 * NG, kSnap = 2;
-    constexpr bool kFine = std::is_same<T, __half>::value;
-    constexpr uint32_t kTile = 2 * L::kBytes;
-    extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t* ring = smem;                                         // [W][NS][kTile]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W * NS * kTile);   // [W][NS]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const Batch& bt = p.a.b;
+// A share: where it begins, and where it ends: the row tile there and the unit of it.
+template <int R> struct Share {
+    Place<R> at;
+    int64_t line, line_end;           // where the row tiles of its begin and its end begin in the line
+    int u_end;
+    int64_t each;
+    int longer, shares;
+    // the first share that begins at `unit` of the line or later
+    __device__ __forceinline__ int from(int64_t unit) const {
+        const int64_t bend = (each + 1) * longer;
+        return unit <= bend ? (int)quotient(unit + each, each + 1) : longer + (int)quotient(unit - bend + each - 1, each);
+    }
+};
 
-    // ------------------------------------------------------------------ the line and its cuts
-    if (lane < NS) ub_init(&bars[warp * NS + lane], 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    __syncwarp();
-    um::pdl_trigger();
-    um::pdl_wait();
+// Share `id` of at most `most`, found by a whole warp; false where there is none.
+template <int R>
+__device__ __forceinline__ bool find_share(const KParams& p, int most, int id, int lane, Share<R>& out) {
+    using P = Place<R>;
+    const Batch& bt = p.a.b;
     auto units_of_head = [&](const Seq& q) -> int64_t {           // length in the line of each kv head of a sequence
         const int nrt = (q.n * p.G + R - 1) / R;
         int64_t sum = 0;
-        for (int t = 0; t < nrt; ++t) sum += kHead + Place<R>::units_of(Place<R>::keys_of(t, q.n, q.len, q.ok, p.G));
+        for (int t = 0; t < nrt; ++t) sum += kHead + P::units_of(P::keys_of(t, q.n, q.len, q.ok, p.G));
         return sum;
     };
     // a lane a sequence, 32 at a time: the units before it and its own
@@ -217,14 +222,14 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
         int64_t m, b;
         total += sequences(s0, m, b);
     }
-    if (total == 0) return;
+    if (total == 0) return false;
     // Equal shares, the first of them one unit longer where they do not divide; no more shares than units.  A cut
     // within kSnap units of a head's end moves to that end: a cut head costs about as much.
-    const int shares = (int)min((int64_t)gridDim.x * W, total), id = blockIdx.x * W + warp;
-    if (id >= shares) return;
+    const int shares = (int)min((int64_t)most, total);
+    if (id >= shares) return false;
     const int64_t each = quotient(total, shares);
     const int longer = (int)(total - each * shares);
-    Place<R> at;                                                  // where the share stands
+    P& at = out.at;                                                 // where the share stands
     int64_t line, line_end;                                       // where its row tile begins in the line; the same of
     int u_end;                                                    // the share's end, and the unit there
     {
@@ -280,9 +285,42 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
         at.rt = __shfl_sync(0xffffffffu, at.rt, 0);
         at.u = __shfl_sync(0xffffffffu, at.u, 0);
     }
-    if (line > line_end || (line == line_end && at.u >= u_end)) return;
+    if (line > line_end || (line == line_end && at.u >= u_end)) return false;
     at.load_seq(p);
     at.load_tile(p);
+    out.line = line;
+    out.line_end = line_end;
+    out.u_end = u_end;
+    out.each = each;
+    out.longer = longer;
+    out.shares = shares;
+    return true;
+}
+
+template <typename T, int NG, int NT, int W, int NS, int MB>
+__global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
+    using L = Blk<NG>;
+    constexpr int R = 8 * NT, DH = 32 * NG;
+    constexpr bool kFine = std::is_same<T, __half>::value;
+    constexpr uint32_t kTile = 2 * L::kBytes;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* ring = smem;                                         // [W][NS][kTile]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W * NS * kTile);   // [W][NS]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const Batch& bt = p.a.b;
+
+    // ------------------------------------------------------------------ the line and its cuts
+    if (lane < NS) ub_init(&bars[warp * NS + lane], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+    um::pdl_trigger();
+    um::pdl_wait();
+    Share<R> sh;
+    if (!find_share(p, gridDim.x * W, blockIdx.x * W + warp, lane, sh)) return;
+    Place<R> at = sh.at;
+    int64_t line = sh.line;
+    const int64_t line_end = sh.line_end;
+    const int u_end = sh.u_end, id = blockIdx.x * W + warp;
     int st = 0;
     uint32_t phase = 0;
     uint8_t* my_ring = ring + warp * NS * kTile;
@@ -688,9 +726,8 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
         const bool whole = u0 == 0 && u1 == at.units;
         uint2 cuts = make_uint2(0u, 0u);                          // from this share on, how many more
         if (u0 == 0 && !whole) {
-            // the shares whose cuts fall inside the head, as the plan above cuts
-            const int64_t unit = line + kHead + at.units - kSnap, bend = (each + 1) * longer;
-            const int past = unit <= bend ? (int)quotient(unit + each, each + 1) : longer + (int)quotient(unit - bend + each - 1, each);
+            // the shares whose cuts fall inside the head, as the plan cuts
+            const int past = sh.from(line + kHead + at.units - kSnap);
             cuts = make_uint2((uint32_t)id, (uint32_t)(past - 1 - id));
         }
         const int slot = 2 * id + (u0 == 0);
