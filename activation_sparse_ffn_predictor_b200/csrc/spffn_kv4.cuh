@@ -23,6 +23,8 @@ template <int NG> struct Blk {
     static __device__ __forceinline__ int vz(int tok, int g) { return vs(tok, g) + 32 * NG; }
 };
 
+constexpr int kMaxLen = 1 << 30;      // positions stay well inside 32 bits, their sums too
+
 // The sequences of a call.
 struct Batch {
     const int32_t *table, *lens, *start;
@@ -47,7 +49,7 @@ __device__ __forceinline__ Seq seq_of(const Batch& b, int s) {
         latch(b.err, ERR_BATCH_ROWS);
         q.n = 0;
     }
-    if (q.len < q.n || (int64_t)q.len > (int64_t)b.width * b.page) {
+    if (q.len < q.n || (int64_t)q.len > (int64_t)b.width * b.page || q.len > kMaxLen) {
         latch(b.err, ERR_BATCH_LEN);
         q.ok = false;
         q.len = 0;

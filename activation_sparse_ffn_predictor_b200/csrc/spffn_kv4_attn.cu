@@ -503,8 +503,8 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                             lds<NG>(v, tile + j * L::kBytes + L::kVs + h * 16 * NG + c * 4 * NG);
 #pragma unroll
                             for (int g = 0; g < NG; g += NG > 4 ? 4 : NG) {
-                                __half2 sum = __hadd2(as_h2(v[g]), as_h2(v[g + 1]));
-                                if constexpr (NG >= 4) sum = __hadd2(sum, __hadd2(as_h2(v[g + 2]), as_h2(v[g + 3])));
+                                __half2 sum = __hadd2(__habs2(as_h2(v[g])), __habs2(as_h2(v[g + 1])));
+                                if constexpr (NG >= 4) sum = __hadd2(sum, __hadd2(__habs2(as_h2(v[g + 2])), __habs2(as_h2(v[g + 3]))));
                                 top = __hmax2_nan(top, sum);
                             }
                         }

@@ -82,10 +82,14 @@ typedef struct {
 typedef struct spffn_mm8_ctx spffn_mm8_ctx;
 
 size_t spffn_mm8_workspace_bytes(const spffn_mm8_config* cfg);
+/* workspace: device, zero-filled before first use, 256-byte aligned, borrowed (int32 parts of tiles that
+ * several SMs share, and their counts). */
 spffn_status spffn_mm8_create(const spffn_mm8_config* cfg, const spffn_mm8_weights* w, void* workspace,
                               size_t workspace_bytes, spffn_mm8_ctx** out);
 spffn_status spffn_mm8_destroy(spffn_mm8_ctx* ctx);
-/* A [T][lda] int8, 16-byte aligned, lda % 16 == 0; a_scale [T]; y [T][ldy]. */
+/* A [T][lda] int8, 16-byte aligned, lda % 16 == 0; a_scale [T]; y [T][ldy].  One kernel: up to 95 tokens
+ * (padded to 16) each weight is read once; from 96 on pairs of SMs share a tile.  Every wait in it is bounded
+ * (2 s); one that runs out latches SPFFN_ERR_TIMEOUT, and _last_device_error makes the context usable again. */
 spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda, const float* a_scale, int32_t T,
                                void* y, int64_t ldy, void* stream);
 spffn_status spffn_mm8_last_device_error(spffn_mm8_ctx* ctx, uint32_t* code, void* stream);
@@ -154,7 +158,7 @@ spffn_status spffn_kv4_destroy(spffn_kv4_ctx* ctx);
  *                    sequence's pages are not read
  * Rows behind q_start[B] (a padded batch) are neither read nor written.  A sequence whose rows
  * do not lie in 0 <= q_start[b] <= q_start[b+1] <= T is skipped; one whose length is below its
- * new tokens or above width page_size is not appended and attends to nothing (its rows of out
+ * new tokens or above width page_size (or 2^30) is not appended and attends to nothing (its rows of out
  * become 0); a page outside [0, pages) is not written, and its tokens are left out of the
  * attention.  Each of these latches SPFFN_ERR_DEVICE_CHECK.
  * Sequences may share pages that only attend reads; two rows of one append must not name the
@@ -172,7 +176,9 @@ spffn_status spffn_kv4_append(spffn_kv4_ctx* ctx, const void* q, int64_t ldq, co
 /* attend: for each new token (position p of its sequence) and query head h, over the cached
  * keys and values of kv head h / (nh / kvh) at positions 0..p:
  *   out = sum_j softmax_j(scale q . K_j) V_j        (fp32 sums and statistics, one rounding)
- * q [T][ldq] as append left it in q_out, out [T][ldo].  A row with nothing to attend to gives 0. */
+ * q [T][ldq] as append left it in q_out, out [T][ldo] (not q).  A row with nothing to attend to gives 0; a row
+ * whose q, or a key or value it sees, is not a number gives NaN, and no other row does.  Two kernels; the
+ * same inputs give the same bits. */
 spffn_status spffn_kv4_attend(spffn_kv4_ctx* ctx, const void* q, int64_t ldq, int32_t T, const int32_t* table,
                               int64_t ld_table, int32_t width, const int32_t* lens, const int32_t* q_start, int32_t B,
                               float scale, void* out, int64_t ldo, void* stream);

@@ -453,6 +453,120 @@ def test_attend_shared_pages_and_a_wide_table():
     c.check_attend(q, out)
 
 
+def test_attend_steps_of_either_sign():
+    """The value is code step + zero, whatever the step's sign: a pool that was not filled by append."""
+    c = Paged([90, 33], [1, 1], 4, 2, 128, 16, "f16", seed=31)
+    c.fill(v_scale=300.0)
+    flip = np.where(c.r.random(c.V[1].shape) < 0.5, -1, 1).astype(np.float16)
+    c.V = (c.V[0], (c.V[1] * flip).astype(np.float16), c.V[2])
+    c.cache.pool.copy_(dev(OB.write_pool(c.K, c.V, c.page, c.kvh, c.dh).reshape(-1)))
+    q = c.rows(4, 2.0)
+    out = torch.empty_like(q)
+    c.cache.attend(q, c.gtable, c.glens, None, out)
+    # a rounding of p s and one of p on numbers up to 15 |step| + |zero| (positions behind the sequences hold NaN)
+    wide = np.nanmax(np.abs(c.V[1]).astype(np.float64))
+    for b in range(2):
+        K, _ = c.of_sequence(b, c.K)
+        V, _ = c.of_sequence(b, c.V)
+        for h in range(2):
+            o, _ = OB.attend(f64(q)[b, 2 * h:2 * h + 2], K[:, h], V[:, h], np.ones((2, c.lens[b]), bool), 128 ** -0.5)
+            within(f64(out)[b, 2 * h:2 * h + 2], o, 2 * HALF["f16"] * (15 * wide + 2000) + HALF["f16"] * np.abs(o))
+
+
+def test_attend_empty_and_padded_calls():
+    c = Paged([20, 30], [1, 1], 4, 2, 64, 16, "bf16", seed=32, pad_rows=3)
+    c.fill()
+    q = c.rows(4)
+    out = torch.full_like(q, 4.0)
+    c.cache.attend(q, c.gtable, c.glens, None, out)            # five rows, two sequences of one token
+    c.check_attend(q, out)
+    assert (out[2:] == 4).all()
+    before = out.clone()
+    c.cache.attend(q[:0], c.gtable, c.glens, torch.zeros(3, dtype=torch.int32, device="cuda"), out[:0])
+    c.cache.attend(q, c.gtable[:0], c.glens[:0], torch.zeros(1, dtype=torch.int32, device="cuda"), out)
+    c.cache.attend(q, c.gtable, c.glens, torch.zeros(3, dtype=torch.int32, device="cuda"), out)      # no new tokens at all
+    c.cache.append(q[:0], q[:0, :2], q[:0, :2], c.gtable, c.glens, torch.zeros(3, dtype=torch.int32, device="cuda"), out[:0])
+    assert torch.equal(out, before) and c.cache.last_device_error() == (sp.OK, 0)
+    c.glens[0] = 2 ** 31 - 1                                   # past what positions may reach
+    c.cache.attend(q, c.gtable, c.glens, None, out)
+    assert (out[0] == 0).all() and torch.equal(out[1], before[1]) and c.cache.last_device_error()[0] == sp.ERR_DEVICE_CHECK
+
+
+@pytest.mark.parametrize("B", [33, 200])
+def test_attend_many_sequences(B):
+    """More sequences than a warp has lanes, some without new tokens, lengths from 1 on."""
+    r = np.random.default_rng(B)
+    lens = r.integers(1, 90, B).tolist()
+    new = [int(x) if r.random() < 0.8 else 0 for x in np.minimum(lens, r.integers(1, 4, B))]
+    c = Paged(lens, new, 4, 2, 64, 16, "bf16", seed=B)
+    c.fill()
+    q = c.rows(4, 2.0)
+    out = torch.full_like(q, math.nan)
+    c.cache.attend(q, c.gtable, c.glens, c.gstart, out)
+    c.check_attend(q, out)
+
+
+def test_two_contexts_at_once_and_a_graph_beside_eager_calls():
+    """Two caches on two streams, and one cache whose captured call is replayed between eager ones on its stream."""
+    cs = [Paged([700, 60], [1, 1], 8, 2, 128, 64, "f16", seed=40 + i) for i in range(2)]
+    for c in cs:
+        c.fill()
+    qs = [c.rows(8, 2.0) for c in cs]
+    outs, streams = [torch.empty_like(q) for q in qs], [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, q, o, s in zip(cs, qs, outs, streams):
+            c.cache.attend(q, c.gtable, c.glens, None, o, stream=s)
+    torch.cuda.synchronize()
+    for c, q, o in zip(cs, qs, outs):
+        c.check_attend(q, o)
+    c, q = cs[0], qs[0]
+    captured, eager = torch.empty_like(q), torch.empty_like(q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.cache.attend(q, c.gtable, c.glens, None, captured)
+        c.cache.attend(q, c.gtable, c.glens, None, captured)
+    for _ in range(3):
+        captured.zero_()
+        eager.zero_()
+        c.cache.attend(q, c.gtable, c.glens, None, eager)
+        g.replay()
+        c.cache.attend(q, c.gtable, c.glens, None, eager)
+        torch.cuda.synchronize()
+        assert torch.equal(captured, outs[0]) and torch.equal(eager, outs[0])
+
+
+def test_offsets_past_32_bits():
+    """Pages whose bytes lie beyond 4 GiB of the pool: appended, attended to and read."""
+    kvh, dh, page, pages, n = 8, 128, 64, 56000, 100
+    cache = sp.KvCache4(pages, page, kvh, kvh, dh, torch.bfloat16, max_seqs=1, max_tokens=n)
+    assert cache.pool.numel() > 2 ** 32
+    gen = torch.Generator(device="cuda").manual_seed(50)
+    q, k, v = (torch.randn(n, kvh, dh, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(3))
+    ids = [pages - 1, pages - 2]
+    table, lens = torch.tensor([ids], dtype=torch.int32, device="cuda"), torch.tensor([n], dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    cache.append(None, k, v, table, lens, start)
+    out = torch.empty_like(q)
+    cache.attend(q, table, lens, start, out)
+    K, V = (torch.empty(2, page, kvh, dh, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache.read(table[0], K, V)
+    whole = cache.pool.view(pages, -1)
+    got = OB.read_pool(whole[pages - 2:].flip(0).cpu().numpy(), page, kvh, dh)
+    assert (whole[:pages - 2].view(torch.int64).amax() == 0) and cache.last_device_error() == (sp.OK, 0)
+    for name, x, t in (("K", k, K), ("V", v, V)):
+        codes, step, zero = (a.reshape(2 * page, *a.shape[2:])[:n] for a in got[name])
+        for a, b in zip((codes, step, zero), OB.quantise(f64(x).astype(np.float32))):
+            assert np.array_equal(a, b)
+        want = OB.values(codes, step, zero)
+        within(f64(t).reshape(2 * page, kvh, dh)[:n], want, np.abs(want) * (HALF["bf16"] + 2 * F32) + TINY["bf16"])
+    c = Paged.__new__(Paged)
+    c.page, c.nh, c.kvh, c.dh, c.dtype, c.B = page, kvh, kvh, dh, "bf16", 1
+    c.lens, c.new, c.start, c.table = [n], [n], np.array([0, n]), np.array([[0, 1]])
+    c.K, c.V = got["K"], got["V"]
+    c.check_attend(q, out)
+
+
 ROPES = {
     "none": None,
     "half": (10000.0 ** (-np.arange(32) / 32), False, 1.0),
