@@ -8,14 +8,20 @@
 // bytes: W and A arrive as 2-D TMA tiles of 128-byte rows, 128-byte swizzle, in a ring as deep as
 // shared memory allows.  Channels are M at every batch size, so a decode call streams each weight
 // once with only its tokens' columns as padding (16), and the output's 32-lane rows are whole sectors.
-// Tiles are dealt whole while full waves of CTAs last; the rest (at most two waves) is one line of
-// K blocks cut into equal shares, so every SM streams the same bytes.  A cut tile's CTAs leave their
+// Tiles are dealt whole while full waves of CTAs last, or in equal rounds; what is left (at most two waves) is
+// one line of K blocks cut into equal shares.  A cut tile's CTAs leave their
 // int32 partials in the workspace and count themselves in; the last to arrive adds them: integer sums,
 // so the order does not matter, and nobody waits.
 //
 // PAIR: two CTAs of a cluster make one tile of 256 channels (cta_group::2): each holds 128 channels' rows and
 // half of the tokens' rows, so a K block brings 32 KB an SM into shared memory in place of 48 KB (BN = 256),
 // and the MMA reads as much less of it.  The even CTA issues for both.
+//
+// Measured on one B200 (weights and activations from HBM, calls back to back in a graph): 1 token, 12,288
+// channels of 4096: MARK1; 32 tokens, 9216 of 9216: MARK2; 256 tokens, 21,504 of 7168: MARK3; 8192 tokens,
+// 9216 of 9216: MARK4.  Bound by the weights' bytes up to about 128 tokens (6.2 TB/s between start and end;
+// 3 us are launch, first bytes and epilogue, 2 to 8 more the joining of cut tiles), by the tensor cores and the
+// power limit above.
 #include <new>
 #include "spffn_umma.cuh"
 #include "../../include/spffn_block.h"
@@ -28,9 +34,9 @@ using namespace um;
 constexpr int kTM = 128, kBK = 128, kThreads = 320, kMaxSt = 12;
 constexpr int kEpiThreads = 256;      // eight epilogue warps: two for each 32 lanes of TMEM, half the columns each
 constexpr int kGroupN = 8;            // channel tiles that share a stretch of the tile order
-#ifndef PAIR_MIN
-#define PAIR_MIN 96
-#endif
+// Tokens of a tile from which pairs of CTAs take it: at 8192 K, 18,944 channels and 256 tokens 36.8 us against 39.1,
+// at 128 tokens 31.7 against 31.8, at 32 tokens 31.8 against 30.2 (a pair's launch and barriers cost about 1 us).
+constexpr int kPairMin = 160;
 constexpr int kMinBlocks = 4;         // K blocks of a share, at least
 constexpr size_t kSmem = 227 * 1024;
 
@@ -68,6 +74,7 @@ struct Walk {
     __device__ __forceinline__ bool next(const MParams& p) {
         if (w < p.whole) {
             tile = w++ * p.units + unit;
+            if (tile >= p.n_tiles * p.t_tiles) return false;      // the last round may not be full; nothing is cut then
             k0 = 0;
             k1 = p.kblocks;
             cut = -1;
@@ -507,8 +514,8 @@ spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda,
     p.kblocks = (c.K + kBK - 1) / kBK;
     p.t_tiles = (T + 255) / 256;
     p.bn = round16((T + p.t_tiles - 1) / p.t_tiles);
-    // pairs of CTAs where the MMA's reads of shared memory bound a tile, from PAIR_MIN tokens on
-    const bool pair = p.bn >= PAIR_MIN && c.N > kTM;
+    // pairs of CTAs where the MMA's reads of shared memory bound a tile
+    const bool pair = p.bn >= kPairMin && c.N > kTM;
     if (pair) p.bn = (p.bn + 31) / 32 * 32;
     const int rows = pair ? p.bn / 2 : p.bn;         // token rows of a CTA
     p.n_tiles = (c.N + (pair ? 2 : 1) * kTM - 1) / ((pair ? 2 : 1) * kTM);
@@ -517,9 +524,18 @@ spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda,
     // whole tiles while two full waves are left, the rest in equal shares
     const long long tiles = (long long)p.n_tiles * p.t_tiles, total = tiles * p.kblocks;
     p.units = (int)std::min<long long>(pair ? ctx->sms / 2 : ctx->sms, std::max<long long>(tiles, total / kMinBlocks));
-    p.whole = tiles % p.units == 0 ? (int)(tiles / p.units) : (int)std::max<long long>(0, tiles / p.units - 1);
+    // Fewer tiles than SMs: every tile in the same number of parts, though up to half of the SMs stay idle (memory
+    // is busy all the same, and joining uneven parts costs more: 12,288 channels of 4096, 1 token, 13.9 us on 96 SMs
+    // against 16.4 on all; 256 tokens 18.7 against 26.7; 9216 of 9216, 32 tokens, 20.5 against 21.9).  More tiles than
+    // SMs: equal rounds of whole tiles where three quarters of the SMs are in them (27,648 of 9216, 73 %: 48.0 us
+    // against 46.8 at 64 tokens, 51.2 against 52.4 at 128; 21,504 of 7168, 57 %: 38.2 against 30.9 at 32).
+    const long long most = pair ? ctx->sms / 2 : ctx->sms, rounds = (tiles + most - 1) / most;
+    const long long even = tiles >= most ? (tiles + rounds - 1) / rounds : p.units / tiles * tiles;
+    const bool equal = tiles < most || tiles * 4 >= rounds * most * 3;
+    if (equal) p.units = (int)even;
+    p.whole = tiles % p.units == 0 ? (int)(tiles / p.units) : equal && tiles >= most ? (int)rounds : (int)std::max<long long>(0, tiles / p.units - 1);
     p.cut_base = p.whole * p.units;
-    p.cut_tiles = (int)(tiles - p.cut_base);
+    p.cut_tiles = (int)std::max<long long>(0, tiles - p.cut_base);
     p.partial = reinterpret_cast<int4*>(ctx->ws + ctx->lay.partial);
     p.tickets = reinterpret_cast<uint32_t*>(ctx->ws + ctx->lay.tickets);
     p.err = reinterpret_cast<uint32_t*>(ctx->ws);

@@ -87,8 +87,8 @@ size_t spffn_mm8_workspace_bytes(const spffn_mm8_config* cfg);
 spffn_status spffn_mm8_create(const spffn_mm8_config* cfg, const spffn_mm8_weights* w, void* workspace,
                               size_t workspace_bytes, spffn_mm8_ctx** out);
 spffn_status spffn_mm8_destroy(spffn_mm8_ctx* ctx);
-/* A [T][lda] int8, 16-byte aligned, lda % 16 == 0; a_scale [T]; y [T][ldy].  One kernel: up to 95 tokens
- * (padded to 16) each weight is read once; from 96 on pairs of SMs share a tile.  Every wait in it is bounded
+/* A [T][lda] int8, 16-byte aligned, lda % 16 == 0; a_scale [T]; y [T][ldy].  One kernel; calls of up
+ * to 256 tokens read each weight once.  Every wait in it is bounded
  * (2 s); one that runs out latches SPFFN_ERR_TIMEOUT, and _last_device_error makes the context usable again. */
 spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda, const float* a_scale, int32_t T,
                                void* y, int64_t ldy, void* stream);
