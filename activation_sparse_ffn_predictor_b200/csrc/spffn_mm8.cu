@@ -18,8 +18,8 @@
 // and the MMA reads as much less of it.  The even CTA issues for both.
 //
 // Measured on one B200 (weights and activations from HBM, calls back to back in a graph): 1 token, 12,288
-// channels of 4096: MARK1; 32 tokens, 9216 of 9216: MARK2; 256 tokens, 21,504 of 7168: MARK3; 8192 tokens,
-// 9216 of 9216: MARK4.  Bound by the weights' bytes up to about 128 tokens (6.2 TB/s between start and end;
+// channels of 4096: 13.9 us; 32 tokens, 9216 of 9216: 20.5 us; 256 tokens, 21,504 of 7168: 42.8 us; 8192 tokens,
+// 9216 of 9216: 515 us (2.70 P operations/s).  Bound by the weights' bytes up to about 128 tokens (6.2 TB/s between start and end;
 // 3 us are launch, first bytes and epilogue, 2 to 8 more the joining of cut tiles), by the tensor cores and the
 // power limit above.
 #include <new>
@@ -359,15 +359,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
                         }
                         fetch(other, c0 + 64);
                     } else {
-                        for (int o = c_first; o <= c_last; ++o) {
-                            if (o == unit) continue;
-                            fetch(o, c0);
+                        // four parts' loads at a time, 16 columns at a time
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                v[4 * c] += u[c].x;
-                                v[4 * c + 1] += u[c].y;
-                                v[4 * c + 2] += u[c].z;
-                                v[4 * c + 3] += u[c].w;
+                        for (int h = 0; h < 2; ++h) {
+                            if (h && !two) break;
+                            for (int o = c_first; o <= c_last; o += 4) {
+                                int4 w[4][4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const bool there = o + k <= c_last && o + k != unit;
+                                    const int4* from = part_of(there ? o + k : c_first, c0 + 32 * h);
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c) w[k][c] = there ? __ldcg(from + c * kTM) : make_int4(0, 0, 0, 0);
+                                }
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c) {
+                                        v[16 * h + 4 * c] += w[k][c].x;
+                                        v[16 * h + 4 * c + 1] += w[k][c].y;
+                                        v[16 * h + 4 * c + 2] += w[k][c].z;
+                                        v[16 * h + 4 * c + 3] += w[k][c].w;
+                                    }
                             }
                         }
                     }
@@ -529,8 +542,11 @@ spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda,
     // against 16.4 on all; 256 tokens 18.7 against 26.7; 9216 of 9216, 32 tokens, 20.5 against 21.9).  More tiles than
     // SMs: equal rounds of whole tiles where three quarters of the SMs are in them (27,648 of 9216, 73 %: 48.0 us
     // against 46.8 at 64 tokens, 51.2 against 52.4 at 128; 21,504 of 7168, 57 %: 38.2 against 30.9 at 32).
+    // The more columns a tile has, the fewer parts: the last CTA reads the others' (256 channels of 16,384: 12 parts
+    // 9.6 us and 6 parts 11.8 at 1 token; 18.4 and 17.6 at 128; 29.9 and 25.1 at 256).
+    const long long parts = p.bn <= 64 ? 12 : p.bn <= 128 ? 6 : 4;
     const long long most = pair ? ctx->sms / 2 : ctx->sms, rounds = (tiles + most - 1) / most;
-    const long long even = tiles >= most ? (tiles + rounds - 1) / rounds : p.units / tiles * tiles;
+    const long long even = tiles >= most ? (tiles + rounds - 1) / rounds : std::min<long long>(p.units / tiles, parts) * tiles;
     const bool equal = tiles < most || tiles * 4 >= rounds * most * 3;
     if (equal) p.units = (int)even;
     p.whole = tiles % p.units == 0 ? (int)(tiles / p.units) : equal && tiles >= most ? (int)rounds : (int)std::max<long long>(0, tiles / p.units - 1);
