@@ -7,6 +7,7 @@
 #include "spffn_kernels.cuh"
 #include "spffn_fused.cuh"
 #include "spffn_union.cuh"
+#include "spffn_block.cuh"
 
 using namespace spffn;
 

@@ -1,7 +1,6 @@
 // Shared pieces of the paged 4-bit cache: its block format, the batch of a call, the context.
 #pragma once
-#include "spffn_internal.cuh"
-#include "../../include/spffn_block.h"
+#include "spffn_block.cuh"
 
 namespace spffn {
 namespace kv4 {

@@ -24,7 +24,7 @@
 // power limit above.
 #include <new>
 #include "spffn_umma.cuh"
-#include "../../include/spffn_block.h"
+#include "spffn_block.cuh"
 
 namespace spffn {
 namespace {

@@ -10,8 +10,7 @@
 // Bound by the bytes of x, y, x_out and q at many rows (8192 rows of 7168, bf16: 79 us, 5.2 TB/s of the 6.56 that a
 // copy reaches; reading a row twice took 240), by latency at few (32 rows of 9216: 3.9 us, one block a row).
 #include <cmath>
-#include "spffn_internal.cuh"
-#include "../../include/spffn_block.h"
+#include "spffn_block.cuh"
 
 namespace spffn {
 namespace {
