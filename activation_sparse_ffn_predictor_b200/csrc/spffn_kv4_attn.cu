@@ -471,7 +471,8 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
         for (int u = u0; u < u1 && !failed; ++u) {
             const uint8_t* tile = my_ring + st * kTile;
             const uint32_t have = 3u & ~(lacks >> (2 * st));
-            if (!ub_try(&my_bar[st], phase)) {
+            // lanes may see the copies' arrival at different tries: they agree before they part
+            if (!__all_sync(0xffffffffu, ub_try(&my_bar[st], phase))) {
                 const unsigned long long t0 = now_ns();
                 while (!ub_try(&my_bar[st], phase)) {
                     if (now_ns() - t0 > um::kUWaitNs) {

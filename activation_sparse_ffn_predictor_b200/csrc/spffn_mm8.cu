@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
                     int4* mine = p.partial + (size_t)((2 * unit + (w.k0 == 0)) * kSides + rank) * (BN / 4) * kTM + row;
                     for (int c0 = 16 * side; c0 < cols; c0 += 32) {
                         int v[16];
+                        __syncwarp();                            // tcgen05.ld is the whole warp's
                         tmem_ld16i(taddr + c0, v);
                         tmem_wait_ld();
 #pragma unroll
@@ -346,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
                 for (int c0 = 16 * side; c0 < cols; c0 += 64) {
                     int v[32];
                     const bool two = c0 + 32 < cols;
+                    __syncwarp();
                     tmem_ld16i(taddr + c0, v);
                     if (two) tmem_ld16i(taddr + c0 + 32, v + 16);
                     tmem_wait_ld();
