@@ -19,7 +19,7 @@
 // rounding lost, so that one is left, and V's codes enter as n - 8 (one fp16 operation a pair): the matrix
 // instructions cut their sums off rather than round them, and over 100,000 positions that showed as 5e-4
 // of the small difference of two large sums.  Measured against 64 bits: 2.9e-4, of which the output's
-// rounding is 2.1e-4; 6e-4 the other way, and 4 us of 39 faster.  Probabilities are kept as
+// rounding is 2.1e-4; 6e-4 the other way, which took 39 us in place of 43.5.  Probabilities are kept as
 // 2^(7 - R) p and up to 2^8 more before the reference moves, R an exponent above every V step seen, so
 // that p s stays in fp16's range.
 //
@@ -34,6 +34,11 @@
 // query rows, blocks that unpack 64 positions into shared memory for 64 rows in the usual layout, rows as
 // M, 132 us against 138 at 256 new tokens over 8205 positions, 32 heads of 64 over 8: unpacking is a small
 // part there, arithmetic on scores and its latency the large one.)
+//
+// Measured on one B200: 32 sequences of about 1400 positions, 72 heads, bf16, 117.5 us (4.4 TB/s; 256 MB more
+// take 45 us more, 54 in the fp16 form); one sequence of 100,003, 32 heads over 8, fp16, 43.5 us; 70 new tokens of 16 sequences of about
+// 4000, 56 heads over 8, bf16, 66 us.  Bound by instructions: about 650 for a unit of one tile of 8 rows, of
+// which 176 unpack codes, 12 warps an SM; then by fixed steps, about 18 us in all, of which the join is 4.
 #include <type_traits>
 #include "spffn_umma.cuh"
 #include "spffn_kv4.cuh"
@@ -49,8 +54,10 @@ using um::ub_init;
 using um::ub_try;
 
 constexpr int kUnit = 32;             // positions of a unit
-constexpr int kSnap = 2;              // a cut as near as that to a head's end moves there
-constexpr int kHead = 1;              // what a head costs beside its units, in units: its q, its sums, its rows
+// What a head costs beside its units, in units: its q, its sums, its rows.  Counted in the line, so that shares with
+// more heads get fewer units: 118.4 us against 120.9 without at 32 sequences of 1400 positions, 72 heads.  (Moving cuts
+// near a head's end to that end, 2 units at most, took 119.2 against 117.5, and 25.6 against 21.1 at 32 sequences of 256.)
+constexpr int kHead = 1;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct KParams {
@@ -223,8 +230,7 @@ __device__ __forceinline__ bool find_share(const KParams& p, int most, int id, i
         total += sequences(s0, m, b);
     }
     if (total == 0) return false;
-    // Equal shares, the first of them one unit longer where they do not divide; no more shares than units.  A cut
-    // within kSnap units of a head's end moves to that end: a cut head costs about as much.
+    // Equal shares, the first of them one unit longer where they do not divide; no more shares than units.
     const int shares = (int)min((int64_t)most, total);
     if (id >= shares) return false;
     const int64_t each = quotient(total, shares);
@@ -270,12 +276,6 @@ __device__ __forceinline__ bool find_share(const KParams& p, int most, int id, i
             }
             bound = raw - in;
             at.u = max(0, (int)in - kHead);
-            if (at.u <= kSnap) at.u = 0;
-            else if (at.units - at.u <= kSnap) {                  // the next one's begin
-                at.u = 0;
-                bound += kHead + at.units;
-                at.next_pair(p);
-            }
         }
         line = __shfl_sync(0xffffffffu, bound, 0);
         line_end = __shfl_sync(0xffffffffu, bound, 1);
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
         uint2 cuts = make_uint2(0u, 0u);                          // from this share on, how many more
         if (u0 == 0 && !whole) {
             // the shares whose cuts fall inside the head, as the plan cuts
-            const int past = sh.from(line + kHead + at.units - kSnap);
+            const int past = sh.from(line + kHead + at.units);
             cuts = make_uint2((uint32_t)id, (uint32_t)(past - 1 - id));
         }
         const int slot = 2 * id + (u0 == 0);
@@ -924,7 +924,8 @@ cudaError_t go(const spffn_kv4_ctx& c, KParams p, cudaStream_t st) {
     p.many = c.sms * S::shares;
     e = launch_chained(kern, (unsigned)(c.sms * S::MB), 32 * S::W, S::smem, p, st);
     if (e != cudaSuccess) return e;
-    // a row tile is cut into about as many parts as there are warps for it
+    // a row tile is cut into about as many parts as there are warps for it; 16 warps a row where that is 16 or more
+    // (one sequence of 100,003 positions, 32 heads over 8: 43.5 us, 94.3 with one warp a row)
     const int64_t rows = (int64_t)p.a.b.T * p.nh, tiles = std::max<int64_t>(p.a.b.B, (int64_t)p.a.b.T * p.G / (8 * NT)) * p.kvh;
     if (tiles * 16 <= (int64_t)c.sms * S::MB * S::W)
         return launch_chained(k_join<T, NG, 8 * NT, 16>, (unsigned)rows, 512, 0, p, st);
@@ -974,7 +975,8 @@ cudaError_t launch_attend(const spffn_kv4_ctx& c, const AttendArgs& a, cudaStrea
     p.ovec = aligned_to(a.out, 8) && a.ldo % 4 == 0;
     p.head_bytes = (uint32_t)(c.cfg.page_size / 16) * (20u * c.cfg.dh);
     p.page_bytes = p.head_bytes * (uint32_t)c.cfg.kvh;
-    // 8, 16 or 32 query rows a tile, by the rows that a kv head has in the mean
+    // 8, 16 or 32 query rows a tile, by the rows that a kv head has in the mean: more rows share the unpacking, fewer
+    // leave less of a tile empty (256 new tokens, 32 heads of 64 over 8: 138 us with 32 rows a tile, 177 with 16)
     const int64_t rows = ((int64_t)a.b.T + a.b.B - 1) / a.b.B * p.G;
     const int nt = std::min(rows <= 8 ? 1 : rows <= 16 ? 2 : 4, most_rows(c.cfg.dh / 32));
     return c.cfg.dtype == SPFFN_BF16 ? by_width<__nv_bfloat16>(c, p, nt, st) : by_width<__half>(c, p, nt, st);
