@@ -83,7 +83,7 @@ class Mm8Weights(ctypes.Structure):
 class Kv4Config(ctypes.Structure):
     _fields_ = [(k, ctypes.c_int32) for k in ("pages", "page_size", "nh", "kvh", "dh", "max_seqs", "max_tokens", "dtype",
                                                "rope_dim", "rope_interleaved")] + [
-        ("rope_amplitude", ctypes.c_float), ("flags", ctypes.c_uint32)]
+        ("flags", ctypes.c_uint32), ("rope_amplitude", ctypes.c_double)]
 
 
 _lib = None
@@ -682,7 +682,7 @@ class KvCache4:
         self.rope = rope
         self.cfg = Kv4Config(self.pages, self.page_size, self.nh, self.kvh, self.dh, int(max_seqs), int(max_tokens), code,
                              0 if rope is None else 2 * rope.freqs.numel(), rope is not None and rope.interleaved,
-                             1.0 if rope is None else rope.amplitude, 0)
+                             0, 1.0 if rope is None else rope.amplitude)
         device = pool.device if pool is not None else torch.device("cuda" if device is None else device)
         with torch.cuda.device(device):
             size = int(library().spffn_kv4_pool_bytes(ctypes.byref(self.cfg)))

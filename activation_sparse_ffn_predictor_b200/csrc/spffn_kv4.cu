@@ -14,7 +14,7 @@ struct AppendParams {
     int64_t ldq, ldk, ldv, ldqo;
     uint8_t* pool;
     const double* freqs;
-    float amp;
+    double amp;
     int nh, kvh, rd, inter;
     Batch b;
 };
@@ -40,23 +40,21 @@ __device__ __forceinline__ float f16_value(float v) {      // rounded to fp16, k
     return __half2float(__float2half_rn(fminf(fmaxf(v, -65504.f), 65504.f)));
 }
 
-// cosine and sine of pos freq: the turns in fp64 (a far position keeps its angle to 2^-53 of the turns), the
-// fraction of a turn as a high and a low fp32 part, the low one by the first term of its series
-__device__ __forceinline__ void angle(int pos, double freq, float amp, float* co, float* si) {
-    double t = (double)pos * freq * 0.15915494309189535;          // 1 / (2 pi)
-    t = 2.0 * (t - rint(t));
-    const float hi = (float)t, lo = (float)(t - (double)hi) * 3.14159265f;
-    float s, c;
-    sincospif(hi, &s, &c);
-    *co = amp * fmaf(-s, lo, c);
-    *si = amp * fmaf(c, lo, s);
+// Cosine and sine of pos freq times the amplitude, in fp64 and rounded once to fp32: codes are decided by the rotated
+// values, and an fp32 sine's last place moved a few of four million of them to the next code.
+__device__ __forceinline__ void angle(int pos, double freq, double amp, float* co, float* si) {
+    const double t = (double)pos * freq * 0.15915494309189535;    // turns: 1 / (2 pi)
+    double s, c;
+    sincospi(2.0 * (t - rint(t)), &s, &c);
+    *co = (float)(amp * c);
+    *si = (float)(amp * s);
 }
 
 // A block takes a row, or a slice of its heads where there are few rows; a thread 8 dims of a head, so a
 // group of 32 dims is four neighbouring lanes and a head 4 NG.  VEC: rows in 16-byte pieces and rotated pairs
 // in whole pieces; otherwise element by element.
 // Bound by latency at few rows (32 rows of 216 heads: 3.6 us) and by instructions at many (4099 rows of 40 + 16
-// heads, half of each rotated: 32 us, 3.3 TB/s; 38 with a division for every code).  Two and four slices a row took 44
+// heads, half of each rotated: 35 us, 3.0 TB/s; 41 with a division for every code).  Two and four slices a row took 44
 // and 56 us there, pieces read ahead of the angles 86 (registers).
 // V codes go out as words put together from two groups' lanes: a head's V codes lie in 8 places, and single
 // halfwords doubled the stores.
@@ -155,7 +153,7 @@ __global__ void __launch_bounds__(256) k_append(const AppendParams p) {
             hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
             bad += __shfl_xor_sync(0xffffffffu, bad, o);
         }
-        const float zero = f16_value(lo), step = bad == 0.f ? f16_value(__fdiv_rn(__fsub_rn(hi, lo), 15.f)) : __int_as_float(0x7fc00000);
+        const float zero = f16_value(lo), step = bad == 0.f ? f16_value(__fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f)) : __int_as_float(0x7fc00000);
         const uint32_t w = pack8(v, step, zero);
         // lane j's word of the V codes: place r = j / (NG / 2), groups 2 (j % (NG / 2)) and the next
         const int r = j / (NG / 2), g2 = 2 * (j % (NG / 2)), from = (lane & ~(LH - 1)) + 4 * g2 + (r >> 1);

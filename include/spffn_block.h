@@ -103,7 +103,7 @@ spffn_status spffn_mm8_last_device_error(spffn_mm8_ctx* ctx, uint32_t* code, voi
  *   512  K steps  [token 16][g NG] fp16,   544  K zeros  [token 16][g NG] fp16
  *   576  V steps  [half 2][c 4][g NG][j 2] fp16,  608  V zeros, the same; token 8 half + 2c + j
  * A cached value is code step + zero.  A group x of 32 dims (fp32) is held as
- *   zero = fp16(min x), step = fp16((max x - min x) / 15), code = clamp(rint((x - zero) / step), 0, 15)
+ *   zero = fp16(min x), step = fp16((max x - min x) (1/15), 1/15 in fp32), code = clamp(rint((x - zero) / step), 0, 15)
  * (code 0 where step = 0); zero and step are clamped to +-65504, and a group that holds a
  * NaN or an infinity gets step = NaN, which every row that attends to it shows.
  * The layout is the one the attention kernel's matrix instructions read without shuffles.
@@ -119,8 +119,8 @@ spffn_status spffn_mm8_last_device_error(spffn_mm8_ctx* ctx, uint32_t* code, voi
  *   rope_amplitude    factor on cosine and sine (1 unless the scaling asks for another) */
 typedef struct {
     int32_t pages, page_size, nh, kvh, dh, max_seqs, max_tokens, dtype, rope_dim, rope_interleaved;
-    float rope_amplitude;
     uint32_t flags;
+    double rope_amplitude;
 } spffn_kv4_config;
 
 typedef struct spffn_kv4_ctx spffn_kv4_ctx;

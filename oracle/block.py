@@ -48,7 +48,7 @@ def quantise(x, dtype=np.float32):
     lo, hi = u.min(axis=-1), u.max(axis=-1)
     with np.errstate(all="ignore"):
         zero = np.clip(lo, -65504, 65504).astype(np.float16)
-        step = np.clip(((hi - lo) / dtype(15)).astype(dtype), -65504, 65504).astype(np.float16)
+        step = np.clip(((hi - lo) * (dtype(1) / dtype(15))).astype(dtype), -65504, 65504).astype(np.float16)
         step = np.where(np.isfinite(u).all(axis=-1), step, np.float16(np.nan))
         code = np.rint((u - zero.astype(dtype)[..., None]) / step.astype(dtype)[..., None])
     code = np.where((step > 0)[..., None], np.clip(code, 0, 15), 0)

@@ -71,7 +71,7 @@ def test_mm8_refusals():
 
 
 def kv4(pages=4, page=16, nh=8, kvh=2, dh=64, seqs=3, tokens=9, dtype=1, rd=64, inter=0, amp=1.0, flags=0):
-    return sp.Kv4Config(pages, page, nh, kvh, dh, seqs, tokens, dtype, rd, inter, amp, flags)
+    return sp.Kv4Config(pages, page, nh, kvh, dh, seqs, tokens, dtype, rd, inter, flags, amp)
 
 
 def test_kv4_refusals():
