@@ -19,9 +19,13 @@
 // rounding lost, so that one is left, and V's codes enter as n - 8 (one fp16 operation a pair): the matrix
 // instructions cut their sums off rather than round them, and over 100,000 positions that showed as 5e-4
 // of the small difference of two large sums.  Measured against 64 bits: 2.9e-4, of which the output's
-// rounding is 2.1e-4; 6e-4 the other way, which took 39 us in place of 43.5.  Probabilities are kept as
-// 2^(7 - R) p and up to 2^8 more before the reference moves, R an exponent above every V step seen, so
-// that p s stays in fp16's range.
+// rounding is 2.1e-4; 6e-4 the other way, which took 39 us in place of 43.5.
+// Range: both factors of p s are kept near the top of what fp16 holds.  The largest probability stands at 2^11
+// to 2^15 (the reference moves where a score passes that), and the steps of each group of dims are brought to at
+// most 1 by a power of two of their own (at least 1/4 when it was set; the sums of the group move with it, exactly).
+// What the operand loses at its small end is at most 2^-25 a position, 2^-34 of the largest p s and less: over N
+// positions N 2^-34 of 15 steps, however far one key stands out and whatever size the steps have down to 2^-15.
+// Smaller ones (fp16 holds them with few bits) are lifted by 2^15 and no further.
 //
 // Work: a unit is 32 positions of one (sequence, kv head, tile of query rows).  The units of the
 // batch are one line, cut into equal shares, one a warp, which finds it from the lengths on the device (a
@@ -59,6 +63,8 @@ constexpr int kUnit = 32;             // positions of a unit
 // near a head's end to that end, 2 units at most, took 119.2 against 117.5, and 25.6 against 21.1 at 32 sequences of 256.)
 constexpr int kHead = 1;
 constexpr float kLog2e = 1.4426950408889634f;
+// Probabilities: 2^kTop where the reference is set, 2^kMost before it moves (fp16 ends at 2^16).
+constexpr float kTop = 11.f, kMost = 15.f;
 
 struct KParams {
     AttendArgs a;
@@ -163,10 +169,13 @@ template <int R> struct Place {
 
 // The running state of a tile of 8 NT query rows: thread (r, c) = (lane / 4, lane % 4) holds query columns
 // 2c, 2c + 1 of each 8; o[2g + i][.][0, 1] dim 32g + 4r + 2i and [2, 3] dim + 1 of them.  `off`: the
-// exponent that probabilities are taken against, -inf before the first.
+// exponent that probabilities are taken against, -inf before the first; the o of group g hold steps times lift[g].
 template <int NG, int NT> struct State {
     float off[NT][2], l[NT][2], o[2 * NG][NT][4];
+    __half2 lift[NG];                 // the power of two that V steps of a group are multiplied by, twice
     __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) lift[g] = __float2half2_rn(32768.f);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             off[t][0] = off[t][1] = -INFINITY;
@@ -399,7 +408,6 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
         uint32_t qf[NT][NG][4], qs[NT][2];
         float fq[NT][2];
         int pos[NT][2];
-        int vexp = 0;                                             // R: V steps seen are below 2^R
         const int rows = at.n * p.G;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -488,41 +496,36 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
             }
             const int p0 = u * kUnit;
             if (have) {
-                // V steps: their largest exponent, and what must not enter the products: positions past
+                // V steps: the largest of each group, and what must not enter the products: positions past
                 // the last and steps that are not numbers (their rows see that in their scores)
                 uint32_t nan_tok = 0;                             // bit t: position p0 + t has such a step
-                __half2 top = __float2half2_rn(0.f);
+                __half2 top[NG];                                  // of this lane's positions: 2c, 2c + 1 of each 8
                 auto tops = [&]() {
-                    // an upper bound by a factor of 4 at most: sums over groups run beside the integer pipe that
-                    // maxima and masks fill; a sum that overflows is held at R = 16 below
-                    top = __float2half2_rn(0.f);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t v[NG];
+                        lds<NG>(v, tile + (k >> 1) * L::kBytes + L::kVs + (k & 1) * 16 * NG + c * 4 * NG);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t v[NG];
-                            lds<NG>(v, tile + j * L::kBytes + L::kVs + h * 16 * NG + c * 4 * NG);
-#pragma unroll
-                            for (int g = 0; g < NG; g += NG > 4 ? 4 : NG) {
-                                __half2 sum = __hadd2(__habs2(as_h2(v[g])), __habs2(as_h2(v[g + 1])));
-                                if constexpr (NG >= 4) sum = __hadd2(sum, __hadd2(__habs2(as_h2(v[g + 2])), __habs2(as_h2(v[g + 3]))));
-                                top = __hmax2_nan(top, sum);
-                            }
-                        }
+                        for (int g = 0; g < NG; ++g) top[g] = k ? __hmax2_nan(top[g], __habs2(as_h2(v[g]))) : __habs2(as_h2(v[g]));
                     }
+                };
+                auto fits = [&]() {                               // false where one is not a number, too
+                    __half2 m = __hmul2(top[0], s.lift[0]);
 #pragma unroll
-                    for (int o = 1; o < 4; o <<= 1) top = __hmax2_nan(top, as_h2(__shfl_xor_sync(0xffffffffu, as_u(top), o)));
+                    for (int g = 1; g < NG; ++g) m = __hmax2_nan(m, __hmul2(top[g], s.lift[g]));
+                    return __all_sync(0xffffffffu, __hble2(m, __float2half2_rn(1.f)));
                 };
                 const bool edge = p0 + kUnit > at.keys || have != 3u;
                 if (!edge) tops();
-                if (edge || __hisnan(__low2half(top)) || __hisnan(__high2half(top))) {
+                if (edge || !fits()) {
                     uint8_t* w = const_cast<uint8_t*>(tile);
                     uint8_t* blk = w + (lane >> 4) * L::kBytes;   // a lane a position
                     const int tok = lane & 15;
                     const bool here = (have >> (lane >> 4)) & 1u;
                     bool nan = false;
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) nan |= __hisnan(*reinterpret_cast<const __half*>(blk + L::vs(tok, g)));
+                    for (int g = 0; g < NG; ++g)
+                        nan |= (*reinterpret_cast<const uint16_t*>(blk + L::vs(tok, g)) & 0x7c00u) == 0x7c00u;
                     if (nan || !here || p0 + lane >= at.keys) {
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
@@ -535,10 +538,27 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                     nan_tok = __reduce_or_sync(0xffffffffu, nan_tok);
                     __syncwarp();
                     tops();
+                    // a step above what its group is lifted for: lifted to 1/4 .. 1/2 from here on
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        __half2 m = top[g];
+#pragma unroll
+                        for (int o = 1; o < 4; o <<= 1) m = __hmax2(m, as_h2(__shfl_xor_sync(0xffffffffu, as_u(m), o)));
+                        const float v = fmaxf(__low2float(m), __high2float(m)), now = __low2float(s.lift[g]);
+                        if (v * now > 1.f) {                      // v and now are normal in fp32
+                            const float next = __uint_as_float((252u << 23) - (__float_as_uint(v) & 0x7f800000u));   // 2^-2 over v's power of two
+                            const float f = next * __uint_as_float((254u << 23) - __float_as_uint(now));
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    s.o[2 * g][t][i] *= f;
+                                    s.o[2 * g + 1][t][i] *= f;
+                                }
+                            s.lift[g] = __float2half2_rn(next);
+                        }
+                    }
                 }
-                const float vt = fmaxf(__low2float(top), __high2float(top));
-                const int ve = min((int)(__float_as_uint(vt) >> 23) - 126, 16);                 // steps are below 2^ve
-                const int vnew = max(vexp, ve);
 
                 // scores of the unit: position r (and r + 8) of each block of 16, columns 2c, 2c + 1
                 float sc[2][NT][4];
@@ -591,16 +611,15 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                                 else if ((nan_tok >> tok) & 1u) sc[j][t][i] = __int_as_float(0x7fc00000);
                             }
                 }
-                // The reference exponent moves only where a score passes it by more than fp16 has room for
-                // (2^8), or a larger V step needs that room; p is then at most 2^(15 - R).
+                // The reference exponent moves only where a score passes it by more than fp16 has room for.
                 float top_s[NT][2];
-                bool far = vnew > vexp;
+                bool far = false;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         top_s[t][i] = fmaxf(fmaxf(sc[0][t][i], sc[0][t][i + 2]), fmaxf(sc[1][t][i], sc[1][t][i + 2]));
-                        far |= top_s[t][i] > s.off[t][i] + (float)(15 - vexp);
+                        far |= top_s[t][i] > s.off[t][i] + kMost;
                     }
                 if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
@@ -610,8 +629,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                             float m = top_s[t][i];
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                            m = fmaxf(m, s.off[t][i] - (float)(vexp - 7));
-                            const float off = m + (float)(vnew - 7);                    // -inf stays
+                            const float off = fmaxf(m - kTop, s.off[t][i]);             // -inf stays
                             const float f = off == s.off[t][i] ? 1.f : ex2(s.off[t][i] - off);
                             s.off[t][i] = off;
                             s.l[t][i] *= f;
@@ -623,7 +641,6 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                                 s.o[d][t][i + 2] *= f;
                             }
                         }
-                    vexp = vnew;
                 }
                 // probabilities, turned into the second operand of the output's product
                 uint32_t pb[2][NT][2], pl[kFine ? 2 : 1][NT][2];   // and what rounding them lost
@@ -668,14 +685,15 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
                         uint32_t b0[NT], b1[NT];
+                        const __half2 l0 = __hmul2(as_h2(s0[g]), s.lift[g]), l1 = __hmul2(as_h2(s1[g]), s.lift[g]);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             if constexpr (kFine) {
-                                b0[t] = as_u(__hfma2(as_h2(pb[j][t][0]), as_h2(s0[g]), __hmul2(as_h2(pl[j][t][0]), as_h2(s0[g]))));
-                                b1[t] = as_u(__hfma2(as_h2(pb[j][t][1]), as_h2(s1[g]), __hmul2(as_h2(pl[j][t][1]), as_h2(s1[g]))));
+                                b0[t] = as_u(__hfma2(as_h2(pb[j][t][0]), l0, __hmul2(as_h2(pl[j][t][0]), l0)));
+                                b1[t] = as_u(__hfma2(as_h2(pb[j][t][1]), l1, __hmul2(as_h2(pl[j][t][1]), l1)));
                             } else {
-                                b0[t] = as_u(__hmul2(as_h2(pb[j][t][0]), as_h2(s0[g])));
-                                b1[t] = as_u(__hmul2(as_h2(pb[j][t][1]), as_h2(s1[g])));
+                                b0[t] = as_u(__hmul2(as_h2(pb[j][t][0]), l0));
+                                b1[t] = as_u(__hmul2(as_h2(pb[j][t][1]), l1));
                             }
                         }
 #pragma unroll
@@ -717,10 +735,11 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const float z = __shfl_sync(0xffffffffu, oz[t][i], 4 * g + c);
+                    const float back = __uint_as_float((254u << 23) - __float_as_uint(__low2float(s.lift[g])));
 #pragma unroll
                     for (int d = 2 * g; d < 2 * g + 2; ++d) {
-                        s.o[d][t][i] = kFine ? s.o[d][t][i] + z : fmaf(s.o[d][t][i], 16777216.f, z);
-                        s.o[d][t][i + 2] = kFine ? s.o[d][t][i + 2] + z : fmaf(s.o[d][t][i + 2], 1048576.f, z);
+                        s.o[d][t][i] = fmaf(s.o[d][t][i], kFine ? back : 16777216.f * back, z);
+                        s.o[d][t][i + 2] = fmaf(s.o[d][t][i + 2], kFine ? back : 1048576.f * back, z);
                     }
                 }
             }

@@ -354,6 +354,37 @@ def test_attend_ranges(case, dtype):
     c.check_attend(q, out, scale=scale)
 
 
+@pytest.mark.parametrize("n,G", [(1, 1), (3, 4)])
+@pytest.mark.parametrize("v", ["1e-1", "1e-2", "1e-3", "1e-4", "neighbours", "groups"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attend_one_key_stands_out_of_many_small_values(dtype, v, n, G):
+    """1800 sequences over the same 100,003 positions, so that one warp walks tens of thousands of them: one key has most
+    of the weight, each of the others some 1e-6 of it.  V is small as a whole, or differs by 2^10 between neighbouring
+    tokens, or by 2^12 between groups of dims."""
+    L, kvh, dh, page, B = 100003, 1, 128, 64, 1800
+    c = Paged([L], [n], G * kvh, kvh, dh, page, dtype, seed=n + len(v))
+    c.fill(v_scale=float(v) if v[0] == "1" else 0.1)
+    at = c.table[0, 5000 // page], 5000 % page
+    codes, step, zero = c.K                       # the first 32 dims hold nothing but the one key's mark
+    codes[..., :32], step[..., 0], zero[..., 0] = 0, 0, 0
+    zero[at[0], at[1], :, 0] = 4.9                # scale 32 4.9 = 13.9: e^13.9 beside 100,003 times e^0.5
+    if v[0] != "1":
+        step, zero = c.V[1].copy(), c.V[2].copy()
+        small = (slice(None), slice(1, None, 2)) if v == "neighbours" else (slice(None),) * 3 + (1,)
+        for a in (step, zero):
+            a[small] = a[small] * np.float16(2.0 ** (-10 if v == "neighbours" else -12))
+        c.V = c.V[0], step, zero
+    c.cache.pool.copy_(dev(OB.write_pool(c.K, c.V, page, kvh, dh).reshape(-1)))
+    many = sp.KvCache4(c.pages, page, G * kvh, kvh, dh, DT[dtype], max_seqs=B, max_tokens=B * n, pool=c.cache.pool)
+    q = dev(c.r.normal(size=(B * n, G * kvh, dh))).to(DT[dtype])
+    q[..., :32] = 1
+    out = torch.full_like(q, math.nan)
+    start = dev(np.arange(B + 1, dtype=np.int32) * n)
+    many.attend(q, c.gtable.expand(B, -1).contiguous(), c.glens.expand(B).contiguous(), start, out)
+    for b in (0, B // 2, B - 1):
+        c.check_attend(q[b * n:(b + 1) * n], out[b * n:(b + 1) * n])
+
+
 def test_attend_rows_that_are_not_numbers_stay_alone():
     c = Paged([40, 50], [2, 1], 4, 2, 64, 16, "f16", seed=6)
     c.fill()
