@@ -16,8 +16,9 @@
 // q_g enter as a high and a low half.  Probabilities times steps are rounded to fp16.  Where the output
 // is bf16 (its own rounding is 2^-8) the probability is rounded before as well, and the codes of V enter
 // as 0..15, whose sum the zeros take back.  Where it is fp16 (2^-11) a second half carries what the first
-// rounding lost, so that one is left, and V's codes enter as n - 8 (one fp16 operation a pair): the matrix
-// instructions cut their sums off rather than round them, and over 100,000 positions that showed as 5e-4
+// rounding lost, so that one is left, of p s; zeros and 8 steps meet both halves as they are, so values with a large
+// mean keep it (before, with one half and z + 8 s rounded: 6e-4 of the mean over 4 keys, now below fp32's share of
+// the scores).  V's codes enter as n - 8 (one fp16 operation a pair): the matrix instructions cut their sums off rather than round them, and over 100,000 positions that showed as 5e-4
 // of the small difference of two large sums.  Measured against 64 bits: 2.9e-4, of which the output's
 // rounding is 2.1e-4; 6e-4 the other way, which took 39 us in place of 43.5.
 // Range: both factors of p s are kept near the top of what fp16 holds.  The largest probability stands at 2^11
@@ -673,15 +674,18 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                     lds<NG>(s1, blk + L::kVs + 16 * NG + c * 4 * NG);
                     uint32_t z0 = *reinterpret_cast<const uint32_t*>(blk + L::kVz + c * 4 * NG + 4 * (r & (NG - 1)));
                     uint32_t z1 = *reinterpret_cast<const uint32_t*>(blk + L::kVz + 16 * NG + c * 4 * NG + 4 * (r & (NG - 1)));
-                    if constexpr (kFine) {                        // zeros for codes around 8
-                        const int at_s = L::kVs + c * 4 * NG + 4 * (r & (NG - 1));
-                        const __half2 eight = __float2half2_rn(8.f);
-                        z0 = as_u(__hfma2(as_h2(*reinterpret_cast<const uint32_t*>(blk + at_s)), eight, as_h2(z0)));
-                        z1 = as_u(__hfma2(as_h2(*reinterpret_cast<const uint32_t*>(blk + at_s + 16 * NG)), eight, as_h2(z1)));
+                    uint32_t e0 = 0u, e1 = 0u;                    // codes around 8: 8 steps go with the zeros, as rows of their own
+                    if constexpr (kFine) {
+                        const uint8_t* at_s = blk + L::kVs + c * 4 * NG + 4 * (r & (NG - 1));
+                        e0 = *reinterpret_cast<const uint32_t*>(at_s);
+                        e1 = *reinterpret_cast<const uint32_t*>(at_s + 16 * NG);
                     }
-                    if (r >= NG) z0 = z1 = 0u;
+                    if (r >= NG) z0 = z1 = e0 = e1 = 0u;
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) mma(oz[t], z0, 0u, z1, 0u, pb[j][t][0], pb[j][t][1]);
+                    for (int t = 0; t < NT; ++t) {
+                        mma(oz[t], z0, e0, z1, e1, pb[j][t][0], pb[j][t][1]);
+                        if constexpr (kFine) mma(oz[t], z0, e0, z1, e1, pl[j][t][0], pl[j][t][1]);
+                    }
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
                         uint32_t b0[NT], b1[NT];
@@ -732,6 +736,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) s.l[t][i] += __shfl_xor_sync(0xffffffffu, s.l[t][i], o);
+                if constexpr (kFine) oz[t][i] = fmaf(8.f, oz[t][i + 2], oz[t][i]);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const float z = __shfl_sync(0xffffffffu, oz[t][i], 4 * g + c);

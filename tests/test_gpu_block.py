@@ -354,6 +354,34 @@ def test_attend_ranges(case, dtype):
     c.check_attend(q, out, scale=scale)
 
 
+@pytest.mark.parametrize("dh", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attend_values_with_a_mean_far_above_their_spread(dtype, dh):
+    """V around 4 with a spread of 0.01: nearly all of the output comes from the zeros."""
+    c = Paged([1, 2, 3, 4, 7, 33, 300], [1, 1, 2, 1, 1, 3, 1], 4, 2, dh, 16, dtype, seed=17)
+    c.fill(v_scale=0.01)
+    c.V = c.V[0], c.V[1], (c.V[2] + np.float16(4)).astype(np.float16)
+    c.cache.pool.copy_(dev(OB.write_pool(c.K, c.V, c.page, c.kvh, c.dh).reshape(-1)))
+    q = c.rows(4, 0.03)
+    out = torch.empty_like(q)
+    c.cache.attend(q, c.gtable, c.glens, c.gstart, out)
+    step = np.nanmax(c.V[1].astype(np.float64))
+    for b in range(c.B):
+        K, Kw = c.of_sequence(b, c.K)
+        V, Vw = c.of_sequence(b, c.V)
+        r0, n, m = int(c.start[b]), c.new[b], c.lens[b]
+        vis = np.repeat(np.arange(m)[None, :] <= np.arange(m - n, m)[:, None], 2, axis=0)
+        for h in range(2):
+            rows = f64(q)[r0:r0 + n, 2 * h:2 * h + 2].reshape(2 * n, dh)
+            o, _ = OB.attend(rows, K[:, h], V[:, h], vis, dh ** -0.5)
+            # scores as in check_attend.  fp16: p s rounded once, codes around 8 at most 8 of them; bf16: a rounding of
+            # p on the whole value and one of p s on 15 steps
+            ds = dh ** -0.5 * np.abs(rows).sum(1) * Kw[:, h].max() * (dh + 16) * F32 + 2.0 ** -21
+            own = HALF["f16"] * (8 * step if dtype == "f16" else Vw.max() + 15 * step)
+            bar = (2 * ds[:, None] + 2.0 ** -18) * Vw.max() + own + HALF[dtype] * np.abs(o)
+            within(f64(out)[r0:r0 + n, 2 * h:2 * h + 2].reshape(2 * n, dh), o, bar, "sequence %d" % b)
+
+
 @pytest.mark.parametrize("n,G", [(1, 1), (3, 4)])
 @pytest.mark.parametrize("v", ["1e-1", "1e-2", "1e-3", "1e-4", "neighbours", "groups"])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
