@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
     uint64_t* tempty = tfull + 2;          // [2]
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tempty + 2);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 3);
-    int* s_last = reinterpret_cast<int*>(tempty + 4);
+    int* s_lasts = reinterpret_cast<int*>(tempty + 4);       // [2]
     uint64_t* done = tempty + 5;
     float* s_scale = reinterpret_cast<float*>(tempty + 6);   // [2][256]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -282,6 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
             // the tokens' scales, read back four at a time; the barrier below makes them visible, and two buffers
             // keep the tile before
             float* as = s_scale + 256 * ab;
+            // one warp's answer for all eight; a warp may still read it when that one is at the next tile, and the tile
+            // between two uses of a word has a barrier of all of them
+            int* s_last = s_lasts + ab;
             const int et = threadIdx.x - 64;
             as[et] = et < cols ? __ldg(p.a_scale + t0 + et) : 0.f;
             int c_first = 0, c_last = -1;  // the CTAs (or pairs) of a cut tile

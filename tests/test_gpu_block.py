@@ -175,6 +175,26 @@ def test_linear8_largest_sums_are_exact():
     check_mm8(y, A, W, sa, sw, None, "f16")
 
 
+@pytest.mark.parametrize("T,K,N", [
+    # one CTA a tile: a line of cut tiles, two or three of them in a share; equal rounds, the last not full; whole tiles
+    # before the line; several token tiles
+    (32, 400, 128 * 170), (1, 272, 128 * 295 - 7), (48, 272, 128 * 300), (280, 272, 128 * 80 - 50), (250, 272, 100),
+    # pairs of CTAs: the same
+    (256, 400, 256 * 84 - 3), (256, 144, 256 * 140 - 9), (256, 272, 256 * 160), (700, 272, 256 * 28 + 9), (5000, 144, 1408)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_linear8_more_tiles_than_ctas(T, K, N, dtype):
+    """Every CTA goes through several tiles: the ring, both accumulators and the scales go from one to the next."""
+    A, W, sa, sw, b = mm8_data(T, K, N, dtype, True, T + K + N)
+    lin = sp.Linear8(W, sw, b, max_tokens=T, dtype=DT[dtype])
+    y, y2 = (torch.full((T, N), math.nan, dtype=DT[dtype], device="cuda") for _ in range(2))
+    lin.forward(A, sa, y)
+    check_mm8(y, A, W, sa, sw, b, dtype)
+    for _ in range(3):
+        lin.forward(A, sa, y2)
+        assert torch.equal(y, y2)
+    assert lin.last_device_error() == (sp.OK, 0)
+
+
 def test_linear8_strides_streams_and_what_lies_beyond():
     T, K, N = 21, 1024, 1500
     A, W, sa, sw, b = mm8_data(T, K, N, "bf16", True, 5, full=True)
