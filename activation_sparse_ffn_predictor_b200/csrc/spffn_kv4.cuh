@@ -68,6 +68,19 @@ __device__ __forceinline__ int seq_of_row(const Batch& b, int t) {
     return b.start[lo] <= t && t < b.start[lo + 1] ? lo : -1;
 }
 
+// The shares that a row is cut into, as the first of them leaves it for the join: that share, how many more, and the
+// row's place in its tile.
+struct Cuts {
+    uint32_t first, more, in;
+};
+inline __host__ __device__ uint2 pack_cuts(const Cuts& c) { return uint2{c.first | (c.in << 24), c.more}; }
+inline __host__ __device__ Cuts unpack_cuts(uint2 m) { return Cuts{m.x & 0xffffffu, m.y, m.x >> 24}; }
+// Whether they lie in a call of `many` shares of tiles of R rows: after a wait that ran out an entry may be an earlier
+// call's, of another tile height, and its parts would lie behind the workspace.
+inline __host__ __device__ bool cuts_in(const Cuts& c, int many, int R) {
+    return c.first < (uint32_t)many && c.more < (uint32_t)many - c.first && c.in < (uint32_t)R;
+}
+
 struct Layout {
     size_t ctl, meta, part, total;
 };

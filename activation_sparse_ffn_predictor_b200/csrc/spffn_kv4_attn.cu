@@ -749,11 +749,11 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                 }
             }
         const bool whole = u0 == 0 && u1 == at.units;
-        uint2 cuts = make_uint2(0u, 0u);                          // from this share on, how many more
+        Cuts cuts{0u, 0u, 0u};                                    // from this share on, how many more
         if (u0 == 0 && !whole) {
             // the shares whose cuts fall inside the head, as the plan cuts
             const int past = sh.from(line + kHead + at.units);
-            cuts = make_uint2((uint32_t)id, (uint32_t)(past - 1 - id));
+            cuts = Cuts{(uint32_t)id, (uint32_t)(past - 1 - id), 0u};
         }
         const int slot = 2 * id + (u0 == 0);
 #pragma unroll
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                 const int in = t * 8 + 2 * c + i, row = at.rt * R + in;
                 if (row >= rows) continue;
                 const int token = at.row0 + row / p.G, head = at.hk * p.G + row % p.G;
-                if (u0 == 0 && r == 0) p.meta[(int64_t)token * p.nh + head] = make_uint2(cuts.x | ((uint32_t)in << 24), cuts.y);
+                if (u0 == 0 && r == 0) p.meta[(int64_t)token * p.nh + head] = pack_cuts(Cuts{cuts.first, cuts.more, (uint32_t)in});
                 if (whole) {
                     T* to = static_cast<T*>(p.a.out) + (int64_t)token * p.a.ldo + (int64_t)head * DH + 4 * r;
                     const float inv = s.l[t][i] == 0.f ? 0.f : 1.f / s.l[t][i];
@@ -820,9 +820,9 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 32 * WPR) k_join(const KParam
         const Seq q = seq_of(p.a.b, sq);
         if (q.n == 0) return;
     }
-    const uint2 m = p.meta[row];
-    const int first = (int)(m.x & 0xffffffu), in = (int)(m.x >> 24), n = (int)m.y + 1;
-    if (n < 2) return;
+    const Cuts cuts = unpack_cuts(p.meta[row]);
+    if (cuts.more == 0 || !cuts_in(cuts, p.many, R)) return;
+    const int first = (int)cuts.first, in = (int)cuts.in, n = (int)cuts.more + 1;
     float top = -INFINITY, l = 0.f;
     float4 acc[V];
 #pragma unroll

@@ -3,12 +3,14 @@ checks, before anything is enqueued), workspace and pool sizes, rotary frequenci
 the oracle's own pins."""
 import ctypes
 import math
+import subprocess
 
 import numpy as np
 import pytest
 
 import activation_sparse_ffn_predictor_b200 as sp
 import oracle.block as OB
+from activation_sparse_ffn_predictor_b200 import build
 
 F = 1 << 40     # an address that host checks never dereference
 BAD = sp.ERR_INVALID_ARG
@@ -120,6 +122,48 @@ def test_kv4_refusals():
             assert f(*bad) == BAD, bad
     assert lib.spffn_kv4_last_device_error(None, None, None) == BAD
     assert lib.spffn_kv4_destroy(ctx) == sp.OK and lib.spffn_kv4_destroy(None) == sp.OK
+
+
+JOIN = r"""
+#include <cstdio>
+#include <cstdint>
+#include "spffn_kv4.cuh"
+using namespace spffn::kv4;
+int main() {
+    // entries as a call of 1776 shares of 8 rows leaves them, and any bits, read in calls of every shape
+    unsigned long long r = 1, bad = 0, in = 0, lost = 0;
+    for (int many = 1; many <= 148 * 16; many = many * 5 / 4 + 1)
+        for (int R : {8, 16, 32})
+            for (int i = 0; i < 20000; ++i) {
+                r = r * 6364136223846793005ull + 1442695040888963407ull;
+                const uint32_t a = (uint32_t)(r >> 32);
+                r = r * 6364136223846793005ull + 1442695040888963407ull;
+                const uint32_t b = (uint32_t)(r >> 32);
+                const uint2 m = i % 2 ? uint2{a, b >> (b & 31)} : pack_cuts(Cuts{a % 1776, b % 200, (a >> 16) % 8});
+                const Cuts c = unpack_cuts(m);
+                const bool ok = cuts_in(c, many, R);
+                // the parts are [2 many][R rows]: share s has places 2 s and 2 s + 1
+                const bool inside = (unsigned long long)c.first + c.more < (unsigned long long)many && c.in < (uint32_t)R;
+                bad += ok && !inside;
+                lost += inside && !ok;
+                in += ok;
+            }
+    for (uint32_t first : {0u, 1u, 1775u, 0xffffffu})
+        for (uint32_t place : {0u, 7u, 31u, 255u}) {
+            const Cuts c = unpack_cuts(pack_cuts(Cuts{first, 9u, place}));
+            bad += c.first != first || c.more != 9u || c.in != place;
+        }
+    std::printf("%llu %llu %d\n", bad, lost, in > 1000);
+}
+"""
+
+
+def test_join_stays_inside_the_workspace(tmp_path):
+    """Whatever an entry holds, the join follows it only to parts that the call's workspace has."""
+    src, exe = tmp_path / "join.cu", tmp_path / "join"
+    src.write_text(JOIN)
+    subprocess.check_call([build.NVCC, "-std=c++17", "--expt-relaxed-constexpr", "-I", build.CSRC, "-o", str(exe), str(src)])
+    assert subprocess.check_output([str(exe)]).split() == [b"0", b"0", b"1"]
 
 
 def test_binding_refuses_what_is_not_on_the_gpu():
