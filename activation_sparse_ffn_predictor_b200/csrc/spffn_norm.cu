@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(256) k_norm_any(const NParams p) {
         float u = elem(x, i);
         if (NORM && y) u = __fadd_rn(u, elem(y, i));
         const float w = NORM && g ? __fmul_rn(u, DT<T>::f(g[i])) : u;
-        ss += NORM ? u * u : w * 0.f;                      // w 0 is NaN where w is not finite
+        if (NORM) ss += u * u;
+        if (!NORM || g) ss = fmaf(w, 0.f, ss);             // NaN where w is not finite: the maximum drops one
         a = fmaxf(a, fabsf(w));
     }
     row_reduce(ss, a, red);
@@ -151,7 +152,10 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) k_norm_wide(const NParams
                 float gv[8];
                 load8(g + 8 * i, gv);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) u[v][k] = __fmul_rn(u[v][k], gv[k]);
+                for (int k = 0; k < 8; ++k) {
+                    u[v][k] = __fmul_rn(u[v][k], gv[k]);
+                    ss = fmaf(u[v][k], 0.f, ss);           // NaN where w is not finite: the maximum drops one
+                }
             }
         } else {
 #pragma unroll

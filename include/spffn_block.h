@@ -45,7 +45,8 @@ extern "C" {
  *   scale = a rs / 127                             (fp32)
  * so q scale is the normalised row u g rs in 8 bits; q does not depend on rs.  A row of
  * a < 2^-119 (127 / a would overflow) gives q = 0 and scale = 0.  A row that holds a NaN or
- * an infinity, or whose sum of squares overflows fp32, gives q = 0 and scale = NaN.
+ * an infinity in u or in w (a gain that is not finite: every row), or whose sum of squares overflows
+ * fp32, gives q = 0 and scale = NaN.
  * x [T][ldx] storage dtype; y [T][ldy] fp32 if y_f32 else storage dtype; g [d] storage
  * dtype; x_out [T][ldo] (may be x itself, or y where it has the same type and stride;
  * no other overlap); q [T][ldq]; scale [T]; eps > 0, finite. */

@@ -113,6 +113,22 @@ def test_norm_quant_special_rows():
         check_norm(v[6:], None, None, 1e-6, xo[6:], q[6:], s[6:], "bf16")
 
 
+@pytest.mark.parametrize("d", [256, 501, 4096, 8192, 9216])      # every form of the wide path, and the other one
+@pytest.mark.parametrize("gain", [math.nan, math.inf, -math.inf])
+def test_norm_quant_gain_that_is_not_finite(d, gain):
+    """One channel's gain is not a number, or infinite: no row has a maximum, also where the channel itself holds 0."""
+    x = torch.randn(5, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(d)).to(torch.bfloat16)
+    at = d // 3
+    x[1:4, at] = 0
+    x[3] = 0
+    g = torch.ones(d, device="cuda", dtype=torch.bfloat16)
+    g[at] = gain
+    y = torch.zeros(5, d, device="cuda")
+    q, s, xo = torch.full((5, d), 5, dtype=torch.int8, device="cuda"), torch.zeros(5, device="cuda"), torch.empty_like(x)
+    sp.norm_quant(x, y, g, xo, q, s)
+    assert torch.isnan(s).all() and (q == 0).all() and torch.equal(xo, x)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("d", [1, 33, 256, 9216, 20001, 131072])
 def test_quantize_rows(d, dtype):
