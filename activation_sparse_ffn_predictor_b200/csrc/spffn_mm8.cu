@@ -1,7 +1,7 @@
 // Product of 8-bit integer rows and weights with a scale per token and channel (spffn_mm8_forward):
 //   y[t][n] = round( a_scale[t] w_scale[n] sum_k A[t][k] W[n][k] + bias[n] )
-// The 32-bit integer sum is exact (K <= 131072 products of at most 2^14), so any split of K gives
-// the same bits.
+// The 32-bit integer sum is exact (K <= 131072 products of at most 2^14; the one sum of 2^31 is put right at the
+// end), so any split of K gives the same bits.
 //
 // k_mm8: persistent tcgen05 kernel, int8 x int8 into int32 in TMEM.  A tile is 128 channels (the
 // MMA's M: lane = channel) x BN tokens (its N, any multiple of 16 up to 256), K in blocks of 128
@@ -22,6 +22,7 @@
 // 9216 of 9216: 515 us (2.70 P operations/s).  Bound by the weights' bytes up to about 128 tokens (6.2 TB/s between start and end;
 // 3 us are launch, first bytes and epilogue, 2 to 8 more the joining of cut tiles), by the tensor cores and the
 // power limit above.
+#include <climits>
 #include <new>
 #include "spffn_umma.cuh"
 #include "spffn_block.cuh"
@@ -388,6 +389,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm8(const __grid_constant__ MPa
                                     }
                             }
                         }
+                    }
+                    // K = 131072 of -128 times -128 is 2^31, which came round to -2^31 (no sum is that low) and is 2^31 in
+                    // fp32 again as 2^31 - 1
+                    if (p.kblocks == 1024) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) v[c] = v[c] == INT_MIN ? INT_MAX : v[c];
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {

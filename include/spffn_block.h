@@ -62,7 +62,7 @@ spffn_status spffn_quantize_rows(int32_t T, int32_t d, int32_t dtype, const void
 
 /* ---- product of 8-bit integers, scales per token and channel ---------------------------
  *   y[t][n] = round( a_scale[t] w_scale[n] sum_k A[t][k] W[n][k] + bias[n] )
- * The sum is a 32-bit integer (exact: K <= 131072, |A|, |W| <= 128); scales and bias are
+ * The sum is exact for any int8 values (a 32-bit integer, and 2^31 where all of K = 131072 are -128); scales and bias are
  * applied in fp32, one rounding to the storage dtype.
  *   K  inner width; K % 16 == 0, 16 <= K <= 131072
  *   N  channels; 1 <= N <= 262144;  max_tokens 1..1048576 (largest T of a call)

@@ -211,6 +211,20 @@ def test_linear8_more_tiles_than_ctas(T, K, N, dtype):
     assert lin.last_device_error() == (sp.OK, 0)
 
 
+@pytest.mark.parametrize("T,N", [(3, 40), (200, 300)])
+def test_linear8_sum_of_two_to_the_31(T, N):
+    """The one sum that 32 bits with a sign do not hold: 131,072 products of -128 and -128."""
+    K = 131072
+    A, W = torch.full((T, K), -128, dtype=torch.int8, device="cuda"), torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+    A[1], W[1] = 127, 127                            # beside it the most negative sums, and sums next to it
+    A[2, 77] = -127
+    sa, sw = torch.ones(T, device="cuda"), torch.full((N,), 2.0 ** -20, device="cuda")
+    y = torch.empty(T, N, dtype=torch.float16, device="cuda")
+    sp.Linear8(W, sw, None, max_tokens=T, dtype=torch.float16).forward(A, sa, y)
+    check_mm8(y, A, W, sa, sw, None, "f16")
+    assert y[0, 0] == 2048
+
+
 def test_linear8_strides_streams_and_what_lies_beyond():
     T, K, N = 21, 1024, 1500
     A, W, sa, sw, b = mm8_data(T, K, N, "bf16", True, 5, full=True)
