@@ -150,7 +150,7 @@ def library(path: Optional[str] = None):
         "spffn_mm8_destroy": (st, [vp]),
         "spffn_mm8_forward": (st, [vp, vp, i64, vp, i32, vp, i64, vp]),
         "spffn_mm8_last_device_error": (st, [vp, ctypes.POINTER(ctypes.c_uint32), vp]),
-        "spffn_rope_frequencies": (st, [i32, f64, i32, f64, f64, ctypes.POINTER(f64), ctypes.POINTER(f32)]),
+        "spffn_rope_frequencies": (st, [i32, f64, i32, f64, f64, ctypes.POINTER(f64), ctypes.POINTER(f64)]),
         "spffn_kv4_pool_bytes": (sz, [ctypes.POINTER(Kv4Config)]),
         "spffn_kv4_workspace_bytes": (sz, [ctypes.POINTER(Kv4Config)]),
         "spffn_kv4_create": (st, [ctypes.POINTER(Kv4Config), vp, sz, vp, vp, sz, ctypes.POINTER(vp)]),
@@ -643,7 +643,7 @@ ROPE_SCALINGS = ("plain", "linear", "ntk", "parts")
 def rope_frequencies(dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, original_len: float = 0.0):
     """(radians per position of the dim / 2 rotated pairs as a float64 numpy array, amplitude) for the long-context
     scalings of spffn_rope_frequencies: "plain", "linear", "ntk", "parts"."""
-    out, amp = np.empty(max(dim // 2, 1), dtype=np.float64), ctypes.c_float(1.0)
+    out, amp = np.empty(max(dim // 2, 1), dtype=np.float64), ctypes.c_double(1.0)
     if scaling not in ROPE_SCALINGS:
         raise ValueError("scaling must be one of %s" % (ROPE_SCALINGS,))
     _check(library().spffn_rope_frequencies(int(dim), float(base), ROPE_SCALINGS.index(scaling), float(factor), float(original_len),

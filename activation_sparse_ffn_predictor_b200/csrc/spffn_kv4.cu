@@ -263,7 +263,7 @@ using namespace spffn::kv4;
 extern "C" {
 
 spffn_status spffn_rope_frequencies(int32_t rope_dim, double base, int32_t scaling, double factor, double original_len,
-                                    double* out, float* amplitude) {
+                                    double* out, double* amplitude) {
     if (rope_dim < 2 || rope_dim % 2 || !out || !(base > 0) || !std::isfinite(base)) return SPFFN_ERR_INVALID_ARG;
     if (scaling < SPFFN_ROPE_PLAIN || scaling > SPFFN_ROPE_PARTS) return SPFFN_ERR_INVALID_ARG;
     if (scaling != SPFFN_ROPE_PLAIN && !(factor >= 1 && std::isfinite(factor))) return SPFFN_ERR_INVALID_ARG;
@@ -280,7 +280,7 @@ spffn_status spffn_rope_frequencies(int32_t rope_dim, double base, int32_t scali
         }
         out[i] = f;
     }
-    if (amplitude) *amplitude = scaling == SPFFN_ROPE_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+    if (amplitude) *amplitude = scaling == SPFFN_ROPE_PARTS ? 0.1 * std::log(factor) + 1.0 : 1.0;
     return SPFFN_OK;
 }
 

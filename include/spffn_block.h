@@ -137,7 +137,7 @@ typedef struct spffn_kv4_ctx spffn_kv4_ctx;
  * *amplitude (may be NULL) is 1 otherwise.  Pure host function. */
 typedef enum { SPFFN_ROPE_PLAIN = 0, SPFFN_ROPE_LINEAR = 1, SPFFN_ROPE_NTK = 2, SPFFN_ROPE_PARTS = 3 } spffn_rope_scaling;
 spffn_status spffn_rope_frequencies(int32_t rope_dim, double base, int32_t scaling, double factor, double original_len,
-                                    double* out, float* amplitude);
+                                    double* out, double* amplitude);
 
 size_t spffn_kv4_pool_bytes(const spffn_kv4_config* cfg);
 size_t spffn_kv4_workspace_bytes(const spffn_kv4_config* cfg);

@@ -205,6 +205,12 @@ def test_rope_frequencies():
         sp.rope_frequencies(8, scaling="other")
 
 
+def test_rope_amplitude_keeps_its_bits():
+    """The config takes the amplitude as a double, and codes are decided by it: it is not rounded on its way there."""
+    for factor in (1.5, 8.0, 40.0):
+        assert math.isclose(sp.rope_frequencies(64, 10000.0, "parts", factor, 4096.0)[1], 0.1 * math.log(factor) + 1, rel_tol=1e-15)
+
+
 def test_oracle_pool_round_trip():
     r = np.random.default_rng(3)
     for dh, kvh, page in ((64, 3, 16), (128, 1, 32), (256, 2, 16)):
