@@ -525,14 +525,17 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(device: int, stream, name: str, fn, *args):
+def _status(device: int, stream, fn, *args):
     """fn(*args, stream) with `device` current; `stream` defaults to that device's current stream."""
     handle = _stream_now(device) if stream is None else getattr(stream, "cuda_stream", stream)
     if _device_now() == device:
-        status = fn(*args, handle)
-    else:
-        with _T.cuda.device(device):
-            status = fn(*args, handle)
+        return fn(*args, handle)
+    with _T.cuda.device(device):
+        return fn(*args, handle)
+
+
+def _call(device: int, stream, name: str, fn, *args):
+    status = _status(device, stream, fn, *args)
     if status != OK:
         _check(status, name)
 
@@ -633,7 +636,8 @@ class Linear8:
 
     def last_device_error(self, stream=None):
         code = ctypes.c_uint32(0)
-        s = library().spffn_mm8_last_device_error(self.ctx, ctypes.byref(code), _stream(stream))
+        _torch()
+        s = _status(self.device, stream, library().spffn_mm8_last_device_error, self.ctx, ctypes.byref(code))
         return s, int(code.value)
 
 
@@ -776,5 +780,6 @@ class KvCache4:
 
     def last_device_error(self, stream=None):
         code = ctypes.c_uint32(0)
-        s = library().spffn_kv4_last_device_error(self.ctx, ctypes.byref(code), _stream(stream))
+        _torch()
+        s = _status(self.device, stream, library().spffn_kv4_last_device_error, self.ctx, ctypes.byref(code))
         return s, int(code.value)

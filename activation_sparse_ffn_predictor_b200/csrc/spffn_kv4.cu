@@ -395,7 +395,7 @@ spffn_status spffn_kv4_read(spffn_kv4_ctx* ctx, const int32_t* page_ids, int32_t
 }
 
 spffn_status spffn_kv4_last_device_error(spffn_kv4_ctx* ctx, uint32_t* code, void* stream) {
-    if (!ctx) return SPFFN_ERR_INVALID_ARG;
+    if (!ctx || !on_device(ctx->device)) return SPFFN_ERR_INVALID_ARG;
     return take_device_error(ctx->err(), code, stream);
 }
 

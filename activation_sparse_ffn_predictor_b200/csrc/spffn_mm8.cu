@@ -591,7 +591,7 @@ spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda,
 }
 
 spffn_status spffn_mm8_last_device_error(spffn_mm8_ctx* ctx, uint32_t* code, void* stream) {
-    if (!ctx) return SPFFN_ERR_INVALID_ARG;
+    if (!ctx || !on_device(ctx->device)) return SPFFN_ERR_INVALID_ARG;
     const spffn_status s = take_device_error(reinterpret_cast<uint32_t*>(ctx->ws), code, stream);
     // a call that gave up may have left tiles counted in part
     if (s == SPFFN_ERR_TIMEOUT &&

@@ -15,7 +15,8 @@
  * library allocates nothing on the device, `stream` is a cudaStream_t as void*,
  * argument errors return before anything is enqueued, device-side problems are
  * latched in the context's workspace and reported by its _last_device_error.  A
- * context is bound to the device that was current when it was created, is used by
+ * context is bound to the device that was current when it was created (its calls, _last_device_error
+ * among them, are refused where another one is current), is used by
  * one stream at a time, and two contexts (or two captured graphs) that share a
  * workspace must not run concurrently.  A call may be captured in a CUDA graph:
  * lengths, positions and page tables are read on the device at replay.

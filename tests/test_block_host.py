@@ -205,6 +205,61 @@ def test_rope_frequencies():
         sp.rope_frequencies(8, scaling="other")
 
 
+class Recorder:
+    """Stands in for torch and the library where a second device would be needed: what is called, on which device."""
+
+    def __init__(self, current):
+        self.current, self.calls = current, []
+        self.cuda = self
+
+    def device(self, index):
+        outer = self
+
+        class Guard:
+            def __enter__(self):
+                self.before, outer.current = outer.current, index
+
+            def __exit__(self, *_):
+                outer.current = self.before
+        return Guard()
+
+    def __getattr__(self, name):
+        if not name.startswith("spffn_"):
+            raise AttributeError(name)
+        return lambda *a: self.calls.append((name, self.current, a[-1])) or sp.OK
+
+
+@pytest.mark.parametrize("cls", [sp.Linear8, sp.KvCache4])
+def test_device_errors_are_read_on_the_contexts_own_device(cls, monkeypatch):
+    """The error word is read after what was enqueued on the context's device, whichever device is current."""
+    rec = Recorder(0)
+    for name, value in (("_T", rec), ("_lib", rec), ("_device_now", lambda: rec.current), ("_stream_now", lambda d: 100 + d)):
+        monkeypatch.setattr(sp, name, value)
+    obj = cls.__new__(cls)
+    obj.ctx, obj.device = None, 1
+    assert obj.last_device_error() == (sp.OK, 0)
+    assert obj.last_device_error(stream=7) == (sp.OK, 0)
+    (_, at, stream), (_, at2, stream2) = rec.calls
+    assert (at, stream, at2, stream2) == (1, 101, 1, 7) and rec.current == 0
+
+
+def test_device_errors_are_refused_on_another_device():
+    """Here no device is current at all: nothing is enqueued."""
+    lib, ctx, code = sp.library(), ctypes.c_void_p(), ctypes.c_uint32(0)
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("a device is current")
+    c, w = mm8(), sp.Mm8Weights(F, F, F)
+    assert lib.spffn_mm8_create(ctypes.byref(c), ctypes.byref(w), F, lib.spffn_mm8_workspace_bytes(ctypes.byref(c)), ctypes.byref(ctx)) == sp.OK
+    assert lib.spffn_mm8_last_device_error(ctx, ctypes.byref(code), None) == BAD
+    lib.spffn_mm8_destroy(ctx)
+    c = kv4()
+    assert lib.spffn_kv4_create(ctypes.byref(c), F, lib.spffn_kv4_pool_bytes(ctypes.byref(c)), F, F,
+                                lib.spffn_kv4_workspace_bytes(ctypes.byref(c)), ctypes.byref(ctx)) == sp.OK
+    assert lib.spffn_kv4_last_device_error(ctx, ctypes.byref(code), None) == BAD
+    lib.spffn_kv4_destroy(ctx)
+
+
 def test_rope_amplitude_keeps_its_bits():
     """The config takes the amplitude as a double, and codes are decided by it: it is not rounded on its way there."""
     for factor in (1.5, 8.0, 40.0):
