@@ -597,7 +597,7 @@ class Linear8:
         code = {torch.float16: F16, torch.bfloat16: BF16}.get(self.out_dtype)
         if code is None:
             raise TypeError("dtype must be float16 or bfloat16, got %s" % self.out_dtype)
-        _on(self.device, w_scale, bias)
+        _on(self.device, w_scale, bias, workspace)
         self.cfg = Mm8Config(self.K, self.N, self.max_tokens, code, 0)
         self._keep = [W, w_scale, bias]
         self.weights = Mm8Weights(_ptr(W), _ptr(w_scale), _ptr(bias))

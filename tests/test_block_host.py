@@ -243,6 +243,37 @@ def test_device_errors_are_read_on_the_contexts_own_device(cls, monkeypatch):
     assert (at, stream, at2, stream2) == (1, 101, 1, 7) and rec.current == 0
 
 
+def test_linear8_refuses_a_workspace_of_another_device(monkeypatch):
+    torch = pytest.importorskip("torch")
+
+    class Fake:
+        def __init__(self, device, dtype, *shape):
+            self.where, self.dtype, self.shape, self.device, self.is_cuda = device, dtype, shape, "cuda:%d" % device, True
+
+        def get_device(self):
+            return self.where
+
+        def stride(self):
+            return self.shape[1:] + (1,)
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return F
+
+        def numel(self):
+            return self.shape[0]
+
+    rec = Recorder(0)
+    rec.float16, rec.bfloat16, rec.int8, rec.float32 = torch.float16, torch.bfloat16, torch.int8, torch.float32
+    monkeypatch.setattr(sp, "_T", rec)
+    made = lambda where: sp.Linear8(Fake(1, torch.int8, 8, 64), Fake(1, torch.float32, 8), workspace=Fake(where, torch.uint8, 1 << 30))  # noqa: E731
+    assert made(1).device == 1
+    with pytest.raises(ValueError):
+        made(0)
+
+
 def test_device_errors_are_refused_on_another_device():
     """Here no device is current at all: nothing is enqueued."""
     lib, ctx, code = sp.library(), ctypes.c_void_p(), ctypes.c_uint32(0)
