@@ -498,22 +498,25 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
             const int p0 = u * kUnit;
             if (have) {
                 // V steps: the largest of each group, and what must not enter the products: positions past
-                // the last and steps that are not numbers (their rows see that in their scores)
-                uint32_t nan_tok = 0;                             // bit t: position p0 + t has such a step
+                // the last, and steps and zeros that are not finite (rows that see them have it from their scores)
+                uint32_t nan_tok = 0;                             // bit t: position p0 + t has such a step or zero
                 __half2 top[NG];                                  // of this lane's positions: 2c, 2c + 1 of each 8
+                __half2 zs = __float2half2_rn(0.f);               // 0 where zeros are finite, a group a lane of r
                 auto tops = [&]() {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t v[NG];
-                        lds<NG>(v, tile + (k >> 1) * L::kBytes + L::kVs + (k & 1) * 16 * NG + c * 4 * NG);
+                        const uint8_t* from = tile + (k >> 1) * L::kBytes + L::kVs + (k & 1) * 16 * NG + c * 4 * NG;
+                        zs = __hfma2(as_h2(*reinterpret_cast<const uint32_t*>(from + 32 * NG + 4 * (r & (NG - 1)))), __float2half2_rn(0.f), zs);
+                        lds<NG>(v, from);
 #pragma unroll
                         for (int g = 0; g < NG; ++g) top[g] = k ? __hmax2_nan(top[g], __habs2(as_h2(v[g]))) : __habs2(as_h2(v[g]));
                     }
                 };
                 auto fits = [&]() {                               // false where one is not a number, too
-                    __half2 m = __hmul2(top[0], s.lift[0]);
+                    __half2 m = zs;
 #pragma unroll
-                    for (int g = 1; g < NG; ++g) m = __hmax2_nan(m, __hmul2(top[g], s.lift[g]));
+                    for (int g = 0; g < NG; ++g) m = __hmax2_nan(m, __hmul2(top[g], s.lift[g]));
                     return __all_sync(0xffffffffu, __hble2(m, __float2half2_rn(1.f)));
                 };
                 const bool edge = p0 + kUnit > at.keys || have != 3u;
@@ -526,7 +529,8 @@ __global__ void __launch_bounds__(32 * W, MB) k_attend(const KParams p) {
                     bool nan = false;
 #pragma unroll
                     for (int g = 0; g < NG; ++g)
-                        nan |= (*reinterpret_cast<const uint16_t*>(blk + L::vs(tok, g)) & 0x7c00u) == 0x7c00u;
+                        nan |= (*reinterpret_cast<const uint16_t*>(blk + L::vs(tok, g)) & 0x7c00u) == 0x7c00u ||
+                               (*reinterpret_cast<const uint16_t*>(blk + L::vz(tok, g)) & 0x7c00u) == 0x7c00u;
                     if (nan || !here || p0 + lane >= at.keys) {
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {

@@ -479,6 +479,34 @@ def test_attend_rows_that_are_not_numbers_stay_alone():
     assert torch.equal(out[ok], good[ok])
 
 
+@pytest.mark.parametrize("dh,page,G", [(64, 16, 1), (64, 64, 8), (128, 64, 2), (128, 16, 4), (256, 32, 1), (256, 64, 5)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attend_values_that_are_not_finite_reach_only_rows_that_see_them(dtype, dh, page, G):
+    """The last drafted token's key or value holds a NaN or an infinity: the tokens before it do not see it, though they
+    lie in the same tile."""
+    c = Paged([40, 71], [1, 3], 2 * G, 2, dh, page, dtype, seed=18)
+    c.fill(nan_behind=False)
+    q = c.rows(2 * G)
+    good = torch.empty_like(q)
+    c.cache.attend(q, c.gtable, c.glens, c.gstart, good)
+    c.check_attend(q, good)
+    clean = c.cache.pool.clone()
+    at = (c.table[1, 70 // page], 70 % page, 1)            # of the second kv head
+    for which, part, bad in (("V", 1, np.nan), ("V", 1, np.inf), ("V", 1, -np.inf), ("V", 2, np.nan), ("V", 2, np.inf), ("V", 2, -np.inf),
+                             ("K", 1, np.nan), ("K", 2, np.nan)):
+        for g in (0, dh // 32 - 1):
+            K, V = (tuple(a.copy() for a in x) for x in (c.K, c.V))
+            (K if which == "K" else V)[part][at + (g,)] = bad
+            c.cache.pool.copy_(dev(OB.write_pool(K, V, page, 2, dh).reshape(-1)))
+            out = torch.empty_like(q)
+            c.cache.attend(q, c.gtable, c.glens, c.gstart, out)
+            assert torch.isnan(out[3, G:]).all(), (which, part, bad, g)
+            out[3, G:] = good[3, G:]
+            c.check_attend(q, out)
+    c.cache.pool.copy_(clean)
+    assert c.cache.last_device_error() == (sp.OK, 0)
+
+
 @pytest.mark.parametrize("dh,page", [(64, 16), (128, 64), (256, 32)])
 def test_attend_batches_that_are_refused_on_the_device(dh, page):
     """Bad rows, lengths and pages: nothing out of range is touched, the rest of the batch is right, the error is latched."""
