@@ -64,6 +64,10 @@ __global__ void __launch_bounds__(256) k_append(const AppendParams p) {
     constexpr int LH = 4 * NG, DH = 32 * NG;                      // lanes of a head
     __shared__ float cs[DH / 2], sn[DH / 2];
     const int t = blockIdx.x;
+    if (t == p.b.T) {                    // one block past the rows looks the sequences over, those without a row too
+        for (int s = blockIdx.y * blockDim.x + threadIdx.x; s < p.b.B; s += gridDim.y * blockDim.x) seq_of(p.b, s);
+        return;
+    }
     const int s = seq_of_row(p.b, t);
     if (s < 0) return;
     const Seq sq = seq_of(p.b, s);
@@ -335,7 +339,7 @@ spffn_status spffn_kv4_append(spffn_kv4_ctx* ctx, const void* q, int64_t ldq, co
                    c.rope_dim, c.rope_interleaved != 0, batch_of(ctx, T, table, ld_table, width, lens, q_start, B)};
     // slices of a row where the rows alone do not fill the device (8 blocks an SM, two rounds)
     const int items = ((q ? c.nh : 0) + 2 * c.kvh) * (c.dh / 8);
-    const dim3 grid(T, std::max(1, std::min((items + 255) / 256, 16 * ctx->sms / T)));
+    const dim3 grid(T + 1, std::max(1, std::min((items + 255) / 256, 16 * ctx->sms / T)));
     auto row16 = [](const void* x, int64_t ld) { return aligned_to(x, 16) && ld % 8 == 0; };
     const bool vec = row16(q, ldq) && row16(q_out, ldqo) && row16(k, ldk) && row16(v, ldv) && c.rope_dim % (c.rope_interleaved ? 8 : 16) == 0;
     cudaStream_t st = (cudaStream_t)stream;

@@ -833,6 +833,30 @@ def test_append_special_values_and_refusals_on_the_device():
     assert (K[0] == 4).all() and (V[0] == 4).all() and c.cache.last_device_error()[0] == sp.ERR_DEVICE_CHECK
 
 
+def test_append_reports_every_sequence_that_it_refuses():
+    """Sequences whose rows or length make no sense are reported by append too, also where no row of the call is theirs;
+    nothing of them is written, and the others are."""
+    kvh, dh, page = 2, 64, 16
+    c = Paged([20, 40, 3], [1, 1, 1], kvh, kvh, dh, page, "bf16", seed=19)
+    k, v = c.rows(kvh), c.rows(kvh)
+    c.cache.append(None, k, v, c.gtable, c.glens, None)
+    pool = c.cache.pool.clone()
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for start, lens, written in ((i32(0, 5, -3, 2 ** 30), c.glens, ()),        # starts beyond the rows, and falling
+                                 (i32(0, 3, 3, 3), i32(2, 40, 3), ()),         # fewer tokens than new ones
+                                 (i32(2, 1, 2, 3), c.glens, (1, 2)),           # a sequence that begins behind its end
+                                 (i32(0, 1, 1, 2), i32(20, 10 ** 9, 3), (0, 2)),   # no new tokens, but a length past the table
+                                 (i32(0, 1, 1, 2), i32(20, -1, 3), (0, 2))):
+        c.cache.pool.zero_()
+        c.cache.append(None, k, v, c.gtable, lens, start)
+        assert c.cache.last_device_error()[0] == sp.ERR_DEVICE_CHECK, start.tolist()
+        got = c.cache.pool.view(c.pages, -1).ne(0).any(1).cpu()
+        assert got.sum() == len(written) and all(got[c.table[b, (c.lens[b] - 1) // page]] for b in written), start.tolist()
+    c.cache.pool.zero_()
+    c.cache.append(None, k, v, c.gtable, c.glens, i32(0, 1, 2, 3))
+    assert torch.equal(c.cache.pool, pool) and c.cache.last_device_error() == (sp.OK, 0)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("unit", [1.0, 0.25, 2.0 ** -10, 3.0])
 def test_append_codes_at_and_beside_halves(dtype, unit):
