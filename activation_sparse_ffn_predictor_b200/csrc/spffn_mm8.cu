@@ -35,9 +35,11 @@ using namespace um;
 constexpr int kTM = 128, kBK = 128, kThreads = 320, kMaxSt = 12;
 constexpr int kEpiThreads = 256;      // eight epilogue warps: two for each 32 lanes of TMEM, half the columns each
 constexpr int kGroupN = 8;            // channel tiles that share a stretch of the tile order
-// Tokens of a tile from which pairs of CTAs take it: at 8192 K, 18,944 channels and 256 tokens 36.8 us against 39.1,
-// at 128 tokens 31.7 against 31.8, at 32 tokens 31.8 against 30.2 (a pair's launch and barriers cost about 1 us).
-constexpr int kPairMin = 160;
+// Tokens of a tile from which pairs of CTAs take it.  Pairs against single CTAs, us, at 128 / 160 / 176 / 192 / 224 / 256
+// tokens: 18,944 channels of 8192 32.1/32.3 33.5/33.5 34.4/34.3 34.6/34.6 35.4/36.0 36.8/38.9; 9216 of 9216 25.0/24.6
+// 26.2/25.5 26.9/26.5 26.9/26.6 28.2/28.0 29.7/30.8; 21,504 of 7168 35.4/34.8 37.3/36.4 38.4/37.8 38.8/38.8 40.6/40.8
+// 42.7/45.4.  (A pair's launch and barriers cost about 1 us; its smaller traffic into shared memory pays above.)
+constexpr int kPairMin = 192;
 constexpr int kMinBlocks = 4;         // K blocks of a share, at least
 constexpr size_t kSmem = 227 * 1024;
 
@@ -554,8 +556,11 @@ spffn_status spffn_mm8_forward(spffn_mm8_ctx* ctx, const int8_t* A, int64_t lda,
     // against 16.4 on all; 256 tokens 18.7 against 26.7; 9216 of 9216, 32 tokens, 20.5 against 21.9).  More tiles than
     // SMs: equal rounds of whole tiles where three quarters of the SMs are in them (27,648 of 9216, 73 %: 48.0 us
     // against 46.8 at 64 tokens, 51.2 against 52.4 at 128; 21,504 of 7168, 57 %: 38.2 against 30.9 at 32).
-    // The more columns a tile has, the fewer parts: the last CTA reads the others' (256 channels of 16,384: 12 parts
-    // 9.6 us and 6 parts 11.8 at 1 token; 18.4 and 17.6 at 128; 29.9 and 25.1 at 256).
+    // The more columns a tile has, the fewer parts: the last CTA reads the others'.  12 / 6 / 4 parts, us: 256 channels of
+    // 16,384 10.1/12.4/14.9 at 1 token, 13.7/14.9/16.7 at 64, 19.0/18.6/19.5 at 128, 30.7/26.3/25.2 at 256; 512 of 8192
+    // 8.8/9.4/10.5, 12.5/11.9/12.2, 18.0/15.5/14.8, 29.5/23.3/21.3; 2048 of 8192 10.2/10.3/10.8, 13.9/12.9/12.9,
+    // 19.3/16.8/15.7, 31.5/25.9/22.5; 1024 of 4096 7.8/8.1/8.1, 10.8/10.6/9.9, 15.0/14.5/12.5, 24.5/22.7/18.7.  (The
+    // narrow matrix of a long K decides at 64 and 128 tokens, where the wide ones would take 6 and 4: 0.6 to 2 us.)
     const long long parts = p.bn <= 64 ? 12 : p.bn <= 128 ? 6 : 4;
     const long long most = pair ? ctx->sms / 2 : ctx->sms, rounds = (tiles + most - 1) / most;
     const long long even = tiles >= most ? (tiles + rounds - 1) / rounds : std::min<long long>(p.units / tiles, parts) * tiles;

@@ -195,6 +195,7 @@ def test_linear8_largest_sums_are_exact():
     # one CTA a tile: a line of cut tiles, two or three of them in a share; equal rounds, the last not full; whole tiles
     # before the line; several token tiles
     (32, 400, 128 * 170), (1, 272, 128 * 295 - 7), (48, 272, 128 * 300), (280, 272, 128 * 80 - 50), (250, 272, 100),
+    (176, 400, 128 * 170 - 3), (350, 272, 128 * 90),
     # pairs of CTAs: the same
     (256, 400, 256 * 84 - 3), (256, 144, 256 * 140 - 9), (256, 272, 256 * 160), (700, 272, 256 * 28 + 9), (5000, 144, 1408)])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
