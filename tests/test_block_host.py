@@ -274,6 +274,15 @@ def test_linear8_refuses_a_workspace_of_another_device(monkeypatch):
         made(0)
 
 
+def test_read_refuses_what_no_grid_holds():
+    lib, ctx = sp.library(), ctypes.c_void_p()
+    c = kv4(pages=1 << 24, page=256, nh=1024, kvh=1024, dh=256, rd=0)
+    assert lib.spffn_kv4_create(ctypes.byref(c), F, lib.spffn_kv4_pool_bytes(ctypes.byref(c)), None, F,
+                                lib.spffn_kv4_workspace_bytes(ctypes.byref(c)), ctypes.byref(ctx)) == sp.OK
+    assert lib.spffn_kv4_read(ctx, F, 1 << 20, F, F + 4096, None) == BAD       # 2^34 blocks of 16 tokens
+    lib.spffn_kv4_destroy(ctx)
+
+
 def test_device_errors_are_refused_on_another_device():
     """Here no device is current at all: nothing is enqueued."""
     lib, ctx, code = sp.library(), ctypes.c_void_p(), ctypes.c_uint32(0)

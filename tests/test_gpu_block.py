@@ -95,6 +95,16 @@ def test_norm_quant_strides_in_place_and_what_lies_between_rows(d, pad, shift):
         assert (gaps == fill).all() and (whole[:shift] == fill).all()
 
 
+@pytest.mark.parametrize("d", [96, 501, 1024, 4096, 9216])
+def test_norm_quant_sum_in_place_of_the_addend(d):
+    """x_out is y, of the storage type and the same stride."""
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    x, y = (torch.randn(7, d, generator=gen, device="cuda").to(torch.float16) for _ in range(2))
+    q, s, before = torch.empty(7, d, dtype=torch.int8, device="cuda"), torch.empty(7, device="cuda"), y.clone()
+    sp.norm_quant(x, y, None, y, q, s)
+    check_norm(x, before, None, 1e-6, y, q, s, "f16")
+
+
 def test_norm_quant_special_rows():
     d = 512
     x = torch.randn(9, d, device="cuda").to(torch.bfloat16)
@@ -383,6 +393,20 @@ def test_attend_long_and_split(nh, kvh, dh, n, length):
     for _ in range(3):                      # the order of sums is fixed: the same bits
         c.cache.attend(q, c.gtable, c.glens, c.gstart, out2)
         assert torch.equal(out, out2)
+
+
+@pytest.mark.parametrize("nh,kvh,dh,page,n,length", [(4, 1, 128, 64, 1500, 1500), (8, 2, 64, 16, 700, 3001), (2, 2, 256, 32, 300, 1000),
+                                                     (16, 2, 128, 32, 513, 514), (64, 1, 64, 256, 200, 1100)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attend_prompts(nh, kvh, dh, page, n, length, dtype):
+    """Hundreds of new tokens of one sequence, from nothing or over what is cached of it, beside a decoded one."""
+    c = Paged([length, 77], [n, 1], nh, kvh, dh, page, dtype, seed=n)
+    c.fill()
+    q = c.rows(nh, 2.0)
+    out = torch.full_like(q, math.nan)
+    c.cache.attend(q, c.gtable, c.glens, c.gstart, out)
+    c.check_attend(q, out)
+    assert c.cache.last_device_error() == (sp.OK, 0)
 
 
 @pytest.mark.parametrize("case", ["large-q", "tiny-q", "zero-q", "large-v", "tiny-v", "mixed-v", "sharp", "scale-0", "scale-negative"])
