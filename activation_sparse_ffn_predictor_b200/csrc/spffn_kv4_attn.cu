@@ -16,11 +16,12 @@
 // q_g enter as a high and a low half.  Probabilities times steps are rounded to fp16.  Where the output
 // is bf16 (its own rounding is 2^-8) the probability is rounded before as well, and the codes of V enter
 // as 0..15, whose sum the zeros take back.  Where it is fp16 (2^-11) a second half carries what the first
-// rounding lost, so that one is left, of p s; zeros and 8 steps meet both halves as they are, so values with a large
-// mean keep it (before, with one half and z + 8 s rounded: 6e-4 of the mean over 4 keys, now below fp32's share of
-// the scores).  V's codes enter as n - 8 (one fp16 operation a pair): the matrix instructions cut their sums off rather than round them, and over 100,000 positions that showed as 5e-4
-// of the small difference of two large sums.  Measured against 64 bits: 2.9e-4, of which the output's
-// rounding is 2.1e-4; 6e-4 the other way, which took 39 us in place of 43.5.
+// rounding lost, so that one is left, of p s; zeros and 8 steps meet both halves as they are, so values with a
+// large mean keep it (one half, and z + 8 s rounded, lost up to 6e-4 of a mean over 4 keys; 138 us in place of 143
+// for 256 new tokens over 8205 positions).  V's codes enter as n - 8 (one fp16 operation a pair): the matrix
+// instructions cut their sums off rather than round them, and over 100,000 positions that showed as 5e-4 of the small
+// difference of two large sums.  Measured against 64 bits: 2.6e-4 in fp16, of which the output's rounding is 2.1e-4
+// (6e-4 with codes from 0 and two roundings, 4 us less at 100,003 positions); 1.75e-3 and 1.66e-3 in bf16.
 // Range: both factors of p s are kept near the top of what fp16 holds.  The largest probability stands at 2^11
 // to 2^15 (the reference moves where a score passes that), and the steps of each group of dims are brought to at
 // most 1 by a power of two of their own (at least 1/4 when it was set; the sums of the group move with it, exactly).
@@ -40,10 +41,14 @@
 // M, 132 us against 138 at 256 new tokens over 8205 positions, 32 heads of 64 over 8: unpacking is a small
 // part there, arithmetic on scores and its latency the large one.)
 //
-// Measured on one B200: 32 sequences of about 1400 positions, 72 heads, bf16, 117.5 us (4.4 TB/s; 256 MB more
-// take 45 us more, 54 in the fp16 form); one sequence of 100,003, 32 heads over 8, fp16, 43.5 us; 70 new tokens of 16 sequences of about
-// 4000, 56 heads over 8, bf16, 66 us.  Bound by instructions: about 650 for a unit of one tile of 8 rows, of
-// which 176 unpack codes, 12 warps an SM; then by fixed steps, about 18 us in all, of which the join is 4.
+// Measured on one B200: 32 sequences of about 1400 positions, 72 heads, bf16, 120 us (4.3 TB/s); one sequence of
+// 100,003, 32 heads over 8, fp16, 45.4 us; 70 new tokens of 16 sequences of about 4000, 56 heads over 8, bf16, 67.4 us;
+// 256 new tokens over 8205, 32 heads of 64 over 8, fp16, 145 us.  Longer contexts: 32 sequences add 5.1 TB/s in bf16 and
+// 4.2 in fp16 from 700 to 2800 positions each, one sequence 4.6 from 100,003 to 400,000, and the lines through these
+// times begin at 19 and 18 us; one sequence of 1000 positions takes 11.  Bound by instructions: about 680 for a unit of
+// one tile of 8 rows, of which 176 unpack codes, on 12 warps an SM.  Many new tokens: 136 to 168 Tflop/s (bf16, 32 heads of
+// 128 over 8, 1024 to 8192 tokens of 8192 positions), by the same arithmetic on scores and probabilities.  There every warp
+// also walks the row tiles of the batch to find its share, a division each.
 #include <type_traits>
 #include "spffn_umma.cuh"
 #include "spffn_kv4.cuh"

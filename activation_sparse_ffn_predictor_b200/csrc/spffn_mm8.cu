@@ -18,10 +18,11 @@
 // and the MMA reads as much less of it.  The even CTA issues for both.
 //
 // Measured on one B200 (weights and activations from HBM, calls back to back in a graph): 1 token, 12,288
-// channels of 4096: 13.9 us; 32 tokens, 9216 of 9216: 20.5 us; 256 tokens, 21,504 of 7168: 42.8 us; 8192 tokens,
-// 9216 of 9216: 515 us (2.70 P operations/s).  Bound by the weights' bytes up to about 128 tokens (6.2 TB/s between start and end;
-// 3 us are launch, first bytes and epilogue, 2 to 8 more the joining of cut tiles), by the tensor cores and the
-// power limit above.
+// channels of 4096: 13.9 us; 32 tokens, 9216 of 9216: 20.5 us; 256 tokens, 21,504 of 7168: 43 us; 8192 tokens,
+// 9216 of 9216: 515 to 525 us (2.6 to 2.7 P operations/s).  Bound by the weights' bytes up to about 128 tokens: from
+// 12,288 to 73,728 channels of 4096 a token takes 6.6 TB/s more, and the line begins at 6 us (launch, first bytes,
+// epilogue, the joining of cut tiles).  By the joining of cut tiles at 256 tokens (all of 84 tiles on 74 pairs are cut;
+// tensor cores busy 52 % of the time), by the tensor cores (86 %) and the power limit above.
 #include <climits>
 #include <new>
 #include "spffn_umma.cuh"

@@ -10,6 +10,8 @@
  * One block over T tokens of B sequences (x the 16-bit residual stream):
  *   norm_quant(x, y) -> mm8 (q/k/v) -> kv4_append -> kv4_attend -> quantize_rows -> mm8
  *   (output projection) -> norm_quant (residual) -> spffn_step (sparse FFN) -> norm_quant ...
+ * spffn_step takes rows in the storage type: between norm_quant and it the caller multiplies q by scale
+ * (this library has no kernel for that).
  *
  * Conventions are those of spffn.h: device pointers into caller-owned memory, the
  * library allocates nothing on the device, `stream` is a cudaStream_t as void*,
@@ -161,10 +163,11 @@ spffn_status spffn_kv4_destroy(spffn_kv4_ctx* ctx);
  * Rows behind q_start[B] (a padded batch) are neither read nor written.  A sequence whose rows
  * do not lie in 0 <= q_start[b] <= q_start[b+1] <= T is skipped; one whose length is below its
  * new tokens or above width page_size (or 2^30) is not appended and attends to nothing (its rows of out
- * become 0); a page outside [0, pages) is not written, and its tokens are left out of the
+ * become 0, those of q_out stay); a page outside [0, pages) is not written, and its tokens are left out of the
  * attention.  Each of these latches SPFFN_ERR_DEVICE_CHECK.
  * Sequences may share pages that only attend reads; two rows of one append must not name the
- * same place.
+ * same place.  A row belongs to one sequence: where starts that fall back let two claim it, that row's
+ * results are either's or a mixture (nothing out of range is touched).
  *
  * append: q_out = rotated q (storage dtype, fp32 arithmetic; may be q itself with the same
  * stride; q and q_out may both be NULL); k rotated, then k and v quantised, written to the cache.
@@ -177,10 +180,13 @@ spffn_status spffn_kv4_append(spffn_kv4_ctx* ctx, const void* q, int64_t ldq, co
 
 /* attend: for each new token (position p of its sequence) and query head h, over the cached
  * keys and values of kv head h / (nh / kvh) at positions 0..p:
- *   out = sum_j softmax_j(scale q . K_j) V_j        (fp32 sums and statistics, one rounding)
+ *   out = sum_j softmax_j(scale q . K_j) V_j
+ * Scores, maxima, sums and outputs are held in fp32.  To fp16 (2^-11) are rounded: q, scaled by a power of two a
+ * row (a value below 2^-19 of its row's largest may lose bits); each probability times a V step, and for a
+ * bf16 output the probability before that.  The output is rounded once.
  * q [T][ldq] as append left it in q_out, out [T][ldo] (not q).  A row with nothing to attend to gives 0; a row
- * whose q, or a key or value it sees, is not a number gives NaN, and no other row does.  Two kernels; the
- * same inputs give the same bits. */
+ * whose q is not finite, or that sees a key that is not a number or a value that is not finite, gives NaN, and no
+ * other row does.  Two kernels; the same inputs give the same bits. */
 spffn_status spffn_kv4_attend(spffn_kv4_ctx* ctx, const void* q, int64_t ldq, int32_t T, const int32_t* table,
                               int64_t ld_table, int32_t width, const int32_t* lens, const int32_t* q_start, int32_t B,
                               float scale, void* out, int64_t ldo, void* stream);

@@ -457,6 +457,26 @@ def test_attend_values_with_a_mean_far_above_their_spread(dtype, dh):
             within(f64(out)[r0:r0 + n, 2 * h:2 * h + 2].reshape(2 * n, dh), o, bar, "sequence %d" % b)
 
 
+@pytest.mark.parametrize("nh,kvh,dh,page", GEOM)
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attend_steps_that_grow_along_a_sequence(nh, kvh, dh, page, dtype):
+    """V grows by 2^16 from the first position to the last, each group of dims at a level of its own, or falls as much."""
+    c = Paged([300, 77, 300, 40], [1, 5, 2, 40], nh, kvh, dh, page, dtype, seed=nh + dh + 3)
+    c.fill()
+    level = np.zeros(c.V[1].shape, np.int64)
+    for b, n in enumerate(c.lens):
+        p = np.arange(n)
+        e = (-9 + 16 * (p if b != 2 else n - 1 - p) // n)[:, None, None] + (np.arange(dh // 32) * 5 % 7 - 3)
+        level[c.table[b, p // page], p % page] = e
+    f = np.exp2(level).astype(np.float16)
+    c.V = c.V[0], (c.V[1] * f).astype(np.float16), (c.V[2] * f).astype(np.float16)
+    c.cache.pool.copy_(dev(OB.write_pool(c.K, c.V, page, kvh, dh).reshape(-1)))
+    q = c.rows(nh, 2.0)
+    out = torch.full_like(q, math.nan)
+    c.cache.attend(q, c.gtable, c.glens, c.gstart, out)
+    c.check_attend(q, out)
+
+
 @pytest.mark.parametrize("n,G", [(1, 1), (3, 4)])
 @pytest.mark.parametrize("v", ["1e-1", "1e-2", "1e-3", "1e-4", "neighbours", "groups"])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
