@@ -521,6 +521,12 @@ def _vector(t, what: str, dtype, n: int):
     raise ValueError("%s: expected a contiguous [%d], got %s" % (what, n, tuple(t.shape)))
 
 
+def _made(device: int):
+    """What a constructor has put on the current stream is done, so that its calls may go to any stream."""
+    if not _T.cuda.is_current_stream_capturing():
+        _T.cuda.current_stream(device).synchronize()
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -581,6 +587,7 @@ class Linear8:
 
     ``W [N, K]`` int8 CUDA tensor, contiguous, K % 16 == 0; ``w_scale [N]`` fp32; ``bias [N]`` of ``dtype`` or
     None; ``dtype`` (torch.float16 or torch.bfloat16) is the output's type; ``max_tokens`` the most rows of a call.
+    Keep the object until its calls have ended on the streams they were given (the workspace is its own).
     """
 
     def __init__(self, W, w_scale, bias=None, max_tokens: int = 256, dtype=None, workspace=None):
@@ -611,6 +618,7 @@ class Linear8:
             ctx = ctypes.c_void_p()
             _check(library().spffn_mm8_create(ctypes.byref(self.cfg), ctypes.byref(self.weights), _p(workspace),
                                               workspace.numel(), ctypes.byref(ctx)), "spffn_mm8_create")
+            _made(self.device)
         self.ctx = ctx
 
     def close(self):
@@ -670,7 +678,8 @@ class Rope:
 class KvCache4:
     """A paged cache of keys and values in 4 bits (wraps an ``spffn_kv4_ctx``): append with rotary positions, attend,
     read back.  The pool (uint8 CUDA tensor, allocated here when not given) has pages x page_size tokens of kvh heads of
-    dh dims; ``max_seqs`` and ``max_tokens`` bound the sequences and new tokens of a call.
+    dh dims; ``max_seqs`` and ``max_tokens`` bound the sequences and new tokens of a call.  Keep the object until its
+    calls have ended on the streams they were given (pool and workspace are its own).
 
     The batch of a call: ``table [B, width]`` int32 pages of each sequence, ``lens [B]`` int32 lengths with the new
     tokens included, ``start [B + 1]`` int32 first rows of the sequences' new tokens, or None for one token each.
@@ -704,6 +713,7 @@ class KvCache4:
             _check(library().spffn_kv4_create(ctypes.byref(self.cfg), _p(pool), pool.numel() * pool.element_size(),
                                               None if rope is None else rope.freqs.data_ptr(), _p(workspace),
                                               workspace.numel(), ctypes.byref(ctx)), "spffn_kv4_create")
+            _made(self.device)
         self.ctx = ctx
 
     def close(self):

@@ -212,6 +212,15 @@ class Recorder:
         self.current, self.calls = current, []
         self.cuda = self
 
+    def is_current_stream_capturing(self):
+        return False
+
+    def current_stream(self, device):
+        return self
+
+    def synchronize(self):
+        pass
+
     def device(self, index):
         outer = self
 

@@ -259,6 +259,42 @@ def test_linear8_strides_streams_and_what_lies_beyond():
     assert torch.isnan(odd[4]).all() and torch.equal(odd[5:], out[5:T, :N])
 
 
+def test_contexts_are_ready_for_any_stream():
+    """Made while the current stream is busy, used at once on another one: the workspace is clean by then."""
+    T, K, N = 8, 4096, 3000
+    A, W, sa, sw, b = mm8_data(T, K, N, "f16", True, 61)
+    y = torch.full((T, N), math.nan, dtype=torch.float16, device="cuda")
+    page, n = 16, 40
+    lens, table = torch.tensor([n], dtype=torch.int32, device="cuda"), torch.arange(3, dtype=torch.int32, device="cuda").view(1, 3)
+    x, big = torch.randn(1, 2, 64, device="cuda").half(), torch.randn(8192, 8192, device="cuda")
+    K4, V4 = (torch.empty(3, page, 2, 64, dtype=torch.float16, device="cuda") for _ in range(2))
+    makes = (lambda: sp.Linear8(W, sw, b, max_tokens=T), lambda: sp.KvCache4(3, page, 2, 2, 64, torch.float16, 1, 1))
+    side, made = torch.cuda.Stream(), []
+    for make, use in zip(makes, (lambda c: c.forward(A, sa, y, stream=side), lambda c: c.append(None, x, x, table, lens, None, stream=side))):
+        first = make()
+        use(first)                                # the first launch of a kernel may wait for the device
+        torch.cuda.synchronize()
+        if not made:
+            y.fill_(math.nan)
+        sizes = [t.numel() for t in (getattr(first, "pool", x), first.workspace)]
+        del first
+        dirty = [torch.full((n_bytes,), 255, dtype=torch.uint8, device="cuda") for n_bytes in sizes]
+        torch.cuda.synchronize()
+        del dirty                                 # what the allocator hands out next is not clean
+        for _ in range(20):
+            big @ big
+        made.append(make())
+        use(made[-1])
+    lin, cache = made
+    cache.read(table[0], K4, V4, stream=side)
+    side.synchronize()
+    check_mm8(y, A, W, sa, sw, b, "f16")
+    assert lin.last_device_error(side) == (sp.OK, 0) and cache.last_device_error(side) == (sp.OK, 0)
+    V4 = V4.view(-1, 2, 64)
+    # half a step: 32 values of N(0, 1) lie within 8 of one another
+    assert (V4[:n - 1] == 0).all() and (V4[n:] == 0).all() and (V4[n - 1] - x[0]).abs().max() < 0.3
+
+
 def test_linear8_graph_replays_on_new_inputs():
     T, K, N = 8, 2048, 3000
     A, W, sa, sw, b = mm8_data(T, K, N, "f16", True, 6)
