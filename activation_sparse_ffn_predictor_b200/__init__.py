@@ -729,6 +729,8 @@ class KvCache4:
 
     def _heads(self, t, what: str, T: int, heads: int):
         """Row stride of [T, heads, dh] (or [T, heads * dh]) whose rows are contiguous."""
+        if t is None:
+            raise TypeError("%s: expected a tensor, got None" % what)
         if t.dim() == 3:
             ld, head, one = t.stride()
             if t.shape != (T, heads, self.dh) or one != 1 or (head != self.dh and heads > 1):

@@ -309,6 +309,17 @@ def test_device_errors_are_refused_on_another_device():
     lib.spffn_kv4_destroy(ctx)
 
 
+def test_attend_says_that_it_wants_an_output():
+    torch = pytest.importorskip("torch")
+    c = sp.KvCache4.__new__(sp.KvCache4)
+    c.ctx, c.nh, c.kvh, c.dh, c.dtype = None, 2, 1, 64, torch.float16
+    q, i = torch.zeros(1, 2, 64, dtype=torch.float16), torch.zeros(1, 1, dtype=torch.int32)
+    with pytest.raises(TypeError, match="out"):
+        c.attend(q, i, i[0])
+    with pytest.raises(TypeError, match="v"):
+        c.append(None, q[:, :1], None, i, i[0])
+
+
 def test_rope_amplitude_keeps_its_bits():
     """The config takes the amplitude as a double, and codes are decided by it: it is not rounded on its way there."""
     for factor in (1.5, 8.0, 40.0):
